@@ -34,7 +34,7 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(INCLUDE, "gptq.h")]
+    deps = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return all(os.path.getmtime(d) <= t for d in deps)
 
 

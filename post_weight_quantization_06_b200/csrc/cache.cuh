@@ -1,0 +1,398 @@
+// The quantized cache of keys and values (gptq_cache_write, gptq_cache_read).
+//
+// Write: a unit is one group of one head of one token of K or V. A power of two of lanes holds
+// it, eight values each (up to four times eight for groups above 256), between its range and its
+// codes: one pass over the values. Read: a unit is eight values.
+//   int:  s = max((mx - mn) / maxq, 2^-126), z = rint(-mn maxq / (mx - mn)),
+//         c = clamp(rint(x / s + z)), value s (c - z)
+//   e4m3: s = max(max |x| / 448, 2^-126), c = e4m3(x / s), value s c
+// Both are bound by bytes for long calls and by the latency of slot -> data -> store for a
+// decode step; a CTA takes a few whole tokens, so that the slots are looked at once per token.
+#pragma once
+
+#include "serve_common.cuh"
+
+namespace gptq {
+namespace serve {
+
+constexpr int CACHE_THREADS = 256;
+constexpr int CACHE_MAX_TB = 8;      // tokens of a CTA
+constexpr int CACHE_MAX_HD = 65536;  // heads * head_dim: unit numbers stay exact in FastDiv
+
+struct CachePlane {
+    const void *x;         // values (read: null)
+    void *y;               // values (write: null)
+    long long ts, hs;      // strides of x or y in elements
+    unsigned char *codes;
+    float *scales;
+    uint8_t *zeros;
+    int vec;               // x or y takes 16-byte accesses
+};
+
+struct CacheArgs {
+    CachePlane p[2];
+    const int64_t *slots;
+    int32_t *claims;
+    long long n_slots;
+    int tokens, heads, dim, group;  // group: values that share a scale
+    int tb;                         // tokens of a CTA
+    FastDiv per_token, per_plane, per_head, per_group;  // units (see each kernel)
+    int w;                          // lanes of a unit (write)
+};
+
+// ---------------------------------------------------------------------------------------
+// Which token of a call stays in a slot that several of them name: the last. Up to
+// GPTQ_CACHE_UNCLAIMED tokens each CTA compares its own tokens' slots with the later ones (two
+// loads a thread); beyond that the comparisons would outgrow the copy, and the tokens first
+// claim their slots: claims[slot] = the largest token + 1.
+// ---------------------------------------------------------------------------------------
+__global__ void cache_claim_kernel(const int64_t *slots, int tokens, long long n_slots,
+                                   int32_t *claims) {
+    pdl_launch_next();
+    pdl_wait_prev();
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t >= tokens) return;
+    const long long s = slots[t];
+    if (s >= 0 && s < n_slots) atomicMax(&claims[s], t + 1);
+}
+
+// slot[j] of the CTA's tokens t0 + j, or -1 where the token is not written.
+__device__ __forceinline__ void cache_resolve(const CacheArgs &a, int t0, int nt, long long *slot,
+                                              int *beaten) {
+    const int tid = threadIdx.x;
+    if (tid < nt) {
+        const long long s = a.slots[t0 + tid];
+        slot[tid] = s;
+        beaten[tid] = 0;
+        if (s >= a.n_slots) report(GPTQ_ERR_ARG, t0 + tid);
+    }
+    __syncthreads();
+    if (a.claims) {
+        if (tid < nt) {
+            const long long s = slot[tid];
+            if (s >= 0 && s < a.n_slots) {
+                // only the winner clears the claim, so a loser can read its own number never
+                if (*(volatile int32_t *)&a.claims[s] == t0 + tid + 1) a.claims[s] = 0;
+                else beaten[tid] = 1;
+            }
+        }
+    } else {
+        for (int i = t0 + 1 + tid; i < a.tokens; i += CACHE_THREADS) {
+            const long long s = a.slots[i];
+            for (int j = 0; j < nt; ++j)
+                if (i > t0 + j && s == slot[j]) beaten[j] = 1;
+        }
+    }
+    __syncthreads();
+    if (tid < nt && (beaten[tid] || slot[tid] >= a.n_slots)) slot[tid] = -1;
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------------------
+// write
+// ---------------------------------------------------------------------------------------
+constexpr float CACHE_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+
+// Min-max grid of a group: scale, its reciprocal, zero-point. The zero-point's quotient is
+// decided in fp64, where -mn maxq and mx - mn are exact: a symmetric range lies on the border
+// between two zero-points, and fp32 would pick either.
+__device__ __forceinline__ bool cache_grid(float mn, float mx, float maxq, float &s, float &r,
+                                           float &z) {
+    mn = fminf(mn, 0.f);
+    mx = fmaxf(mx, 0.f);
+    if (mx == mn) { mn = -1.f; mx = 1.f; }
+    const float range = mx - mn;
+    if (!finitef(range)) return false;
+    s = fmaxf(__fdiv_rn(range, maxq), SCALE_MIN);
+    r = __frcp_rn(s);
+    const double num = -(double)mn * (double)maxq, den = (double)mx - (double)mn;
+    // near the quotient, then the nearest by the remainder, ties to even
+    int q = (int)rintf(__fdiv_rn(-mn, range) * maxq);
+    const double d = 2.0 * (num - (double)q * den);
+    if (d > den || (d == den && (q & 1))) ++q;
+    else if (d < -den || (d == -den && (q & 1))) --q;
+    z = (float)min(max(q, 0), (int)maxq);
+    return true;
+}
+
+template <typename T, int FMT, int V>
+__global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid_constant__ CacheArgs a) {
+    __shared__ long long slot[CACHE_MAX_TB];
+    __shared__ int beaten[CACHE_MAX_TB];
+    pdl_launch_next();
+    pdl_wait_prev();
+    const int t0 = blockIdx.x * a.tb;
+    const int nt = min(a.tb, a.tokens - t0);
+    const int w = a.w, l = threadIdx.x & (w - 1);
+    const uint32_t units = (uint32_t)nt * a.per_token.d;
+    const uint32_t step = CACHE_THREADS / w;
+    const int nvec = a.group >> 3;
+    cache_resolve(a, t0, nt, slot, beaten);
+    for (uint32_t u0 = 0; u0 < units; u0 += step) {
+        const uint32_t u = u0 + threadIdx.x / w;
+        const bool live = u < units;
+        const uint32_t j = a.per_token.div(live ? u : 0), rem = live ? u - j * a.per_token.d : 0;
+        const uint32_t pl = a.per_plane.div(rem), hg = rem - pl * a.per_plane.d;
+        const uint32_t h = a.per_head.div(hg), g = hg - h * a.per_head.d;
+        const CachePlane &p = a.p[pl];
+        const long long sl = live ? slot[j] : -1;
+        const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
+                     (long long)h * p.hs + (long long)g * a.group;
+        Raw8<T> raw[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = l + i * w;
+            const bool on = sl >= 0 && v < nvec;
+            load8(x + (on ? 8 * v : 0), on && p.vec, on ? 8 : 0, raw[i]);
+        }
+        float s, r, z = 0.f;
+        bool bad;
+        uint32_t top = 0;
+        float mn = 0.f, mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v[8];
+            widen8(raw[i], v);
+            top = max(top, amax_bits8(v));
+            if (FMT != GPTQ_CACHE_E4M3) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) { mn = fminf(mn, v[e]); mx = fmaxf(mx, v[e]); }
+            }
+        }
+        for (int o = w >> 1; o; o >>= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (FMT != GPTQ_CACHE_E4M3) {
+                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            }
+        }
+        bad = top >= INF_BITS;
+        if (FMT == GPTQ_CACHE_E4M3) {
+            if (__any_sync(0xffffffffu, bad)) {
+                top = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float v[8];
+                    widen8(raw[i], v);
+                    top = max(top, amax_finite8(v));
+                }
+                for (int o = w >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            s = e4m3_scale(top);
+            r = __frcp_rn(s);
+        } else {
+            constexpr float maxq = FMT == GPTQ_CACHE_INT4 ? 15.f : 255.f;
+            if (bad || !cache_grid(mn, mx, maxq, s, r, z)) {
+                bad = true;
+                s = __uint_as_float(0x7fffffffu);
+                r = 0.f;
+                z = 0.f;
+            }
+        }
+        if (sl < 0) continue;
+        if (bad && l == 0) report(GPTQ_ERR_NONFINITE, t0 + (int)j);
+        const long long row = sl * a.heads + h;
+        if (l == 0) {
+            const long long m = row * a.per_head.d + g;
+            p.scales[m] = s;
+            if (FMT != GPTQ_CACHE_E4M3) p.zeros[m] = (uint8_t)z;
+        }
+        const long long at = row * a.dim + (long long)g * a.group;  // element of the first code
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = l + i * w;
+            if (v >= nvec) continue;
+            float f[8];
+            widen8(raw[i], f);
+            if (FMT == GPTQ_CACHE_E4M3) {
+                if (bad) amax_finite8(f);
+                *reinterpret_cast<uint2 *>(p.codes + at + 8 * v) = e4m3_codes8(f, r);
+            } else {
+                constexpr float maxq = FMT == GPTQ_CACHE_INT4 ? 15.f : 255.f;
+                uint32_t c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // x r + z rounded once, to a whole number; a group that is not finite has
+                    // r = 0 and gets code 0
+                    const float y = bad ? CACHE_MAGIC : fmaf(f[e], r, CACHE_MAGIC + z);
+                    c[e] = __float_as_uint(fminf(fmaxf(y, CACHE_MAGIC), CACHE_MAGIC + maxq));
+                }
+                if (FMT == GPTQ_CACHE_INT8) {
+                    const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040),
+                                                    __byte_perm(c[2], c[3], 0x0040), 0x5410);
+                    const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040),
+                                                    __byte_perm(c[6], c[7], 0x0040), 0x5410);
+                    *reinterpret_cast<uint2 *>(p.codes + at + 8 * v) = make_uint2(lo, hi);
+                } else {
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) word |= (c[e] & 15u) << (4 * e);
+                    *reinterpret_cast<uint32_t *>(p.codes + (at >> 1) + 4 * v) = word;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// read
+// ---------------------------------------------------------------------------------------
+constexpr int CACHE_READ_UNROLL = 4;
+
+// One unit is eight values; per_token.d units per token over the planes, per_plane.d per plane,
+// per_head.d per head, and per_group.d of them share a scale.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_constant__ CacheArgs a) {
+    __shared__ long long slot[CACHE_MAX_TB];
+    pdl_launch_next();
+    pdl_wait_prev();
+    const int t0 = blockIdx.x * a.tb;
+    const int nt = min(a.tb, a.tokens - t0);
+    if ((int)threadIdx.x < nt) {
+        long long s = a.slots[t0 + threadIdx.x];
+        if (s >= a.n_slots) {
+            report(GPTQ_ERR_ARG, t0 + (int)threadIdx.x);
+            s = -1;
+        }
+        slot[threadIdx.x] = s;
+    }
+    __syncthreads();
+    const uint32_t units = (uint32_t)nt * a.per_token.d;
+    const int groups = a.dim / a.group;
+    for (uint32_t u0 = threadIdx.x; u0 < units; u0 += CACHE_THREADS * CACHE_READ_UNROLL) {
+        uint2 c[CACHE_READ_UNROLL];
+        float s[CACHE_READ_UNROLL], z[CACHE_READ_UNROLL];
+        T *y[CACHE_READ_UNROLL];
+        bool vec[CACHE_READ_UNROLL];
+#pragma unroll
+        for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
+            const uint32_t u = u0 + i * CACHE_THREADS;
+            y[i] = nullptr;
+            vec[i] = false;
+            c[i] = make_uint2(0, 0);
+            s[i] = z[i] = 0.f;
+            if (u >= units) continue;
+            const uint32_t j = a.per_token.div(u), rem = u - j * a.per_token.d;
+            const long long sl = slot[j];
+            if (sl < 0) continue;
+            const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d;
+            const CachePlane &p = a.p[pl];
+            const uint32_t h = a.per_head.div(v);
+            const long long at = sl * a.heads * a.dim + 8LL * v;
+            const long long m = sl * a.heads * groups + a.per_group.div(v);
+            if (FMT == GPTQ_CACHE_INT4)
+                c[i].x = *reinterpret_cast<const uint32_t *>(p.codes + (at >> 1));
+            else
+                c[i] = *reinterpret_cast<const uint2 *>(p.codes + at);
+            s[i] = p.scales[m];
+            if (FMT != GPTQ_CACHE_E4M3) z[i] = (float)p.zeros[m];
+            y[i] = static_cast<T *>(p.y) + (long long)(t0 + (int)j) * p.ts + (long long)h * p.hs +
+                   8LL * (v - h * a.per_head.d);
+            vec[i] = p.vec;
+        }
+#pragma unroll
+        for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
+            if (!y[i]) continue;
+            float f[8];
+            if (FMT == GPTQ_CACHE_E4M3) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = e < 2 ? c[i].x : c[i].y;
+                    uint32_t h2;
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * (e & 1)))));
+                    const __half2 hv = *reinterpret_cast<const __half2 *>(&h2);
+                    f[2 * e] = __low2float(hv) * s[i];
+                    f[2 * e + 1] = __high2float(hv) * s[i];
+                }
+            } else {
+                // a code in the low bits of 2^23 is 2^23 + code: the difference is exact
+                const float bias = 8388608.f + z[i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint32_t q;
+                    if (FMT == GPTQ_CACHE_INT4) q = ((c[i].x >> (4 * e)) & 15u) | 0x4b000000u;
+                    else q = __byte_perm(e < 4 ? c[i].x : c[i].y, 0x4b000000u, 0x7440u | (e & 3));
+                    f[e] = (__uint_as_float(q) - bias) * s[i];
+                }
+            }
+            store8(y[i], vec[i], f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+inline int cache_tokens_per_cta(int tokens) {
+    // enough CTAs for several per SM before a CTA takes more than one token
+    const int want = device_sm_count() * 8;
+    int tb = tokens / want;
+    return tb < 1 ? 1 : tb > CACHE_MAX_TB ? CACHE_MAX_TB : tb;
+}
+
+template <typename T, int FMT>
+inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
+    const int nvec = a.group / 8;
+    a.w = 1;
+    while (a.w < 32 && a.w < nvec) a.w *= 2;
+    const dim3 grid((a.tokens + a.tb - 1) / a.tb);
+    if (nvec <= a.w)
+        return launch_kernel(cache_write_kernel<T, FMT, 1>, grid, dim3(CACHE_THREADS), 0, s, true, a);
+    return launch_kernel(cache_write_kernel<T, FMT, 4>, grid, dim3(CACHE_THREADS), 0, s, true, a);
+}
+template <typename T>
+inline int cache_write_fmt(CacheArgs &a, int format, cudaStream_t s) {
+    switch (format) {
+        case GPTQ_CACHE_INT4: return cache_write_launch<T, GPTQ_CACHE_INT4>(a, s);
+        case GPTQ_CACHE_INT8: return cache_write_launch<T, GPTQ_CACHE_INT8>(a, s);
+        default: return cache_write_launch<T, GPTQ_CACHE_E4M3>(a, s);
+    }
+}
+inline int cache_write(CacheArgs &a, int x_dtype, int format, cudaStream_t s) {
+    const int groups = a.dim / a.group, planes = a.p[1].x ? 2 : 1;
+    a.per_head = fast_div(groups);
+    a.per_plane = fast_div((uint32_t)a.heads * groups);
+    a.per_token = fast_div((uint32_t)planes * a.heads * groups);
+    a.per_group = fast_div(1);
+    a.tb = cache_tokens_per_cta(a.tokens);
+    if (a.tokens > GPTQ_CACHE_UNCLAIMED) {
+        if (int st = launch_kernel(cache_claim_kernel, dim3((a.tokens + 255) / 256), dim3(256), 0, s,
+                                   true, a.slots, a.tokens, a.n_slots, a.claims))
+            return st;
+    } else {
+        a.claims = nullptr;
+    }
+    switch (x_dtype) {
+        case GPTQ_BF16: return cache_write_fmt<__nv_bfloat16>(a, format, s);
+        case GPTQ_F16: return cache_write_fmt<__half>(a, format, s);
+        default: return cache_write_fmt<float>(a, format, s);
+    }
+}
+
+template <typename T>
+inline int cache_read_fmt(CacheArgs &a, int format, cudaStream_t s) {
+    const dim3 grid((a.tokens + a.tb - 1) / a.tb), block(CACHE_THREADS);
+    switch (format) {
+        case GPTQ_CACHE_INT4: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT4>, grid, block, 0, s, true, a);
+        case GPTQ_CACHE_INT8: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT8>, grid, block, 0, s, true, a);
+        default: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_E4M3>, grid, block, 0, s, true, a);
+    }
+}
+inline int cache_read(CacheArgs &a, int y_dtype, int format, cudaStream_t s) {
+    const int planes = a.p[1].y ? 2 : 1;
+    a.per_head = fast_div(a.dim / 8);
+    a.per_plane = fast_div((uint32_t)a.heads * (a.dim / 8));
+    a.per_token = fast_div((uint32_t)planes * a.heads * (a.dim / 8));
+    a.per_group = fast_div(a.group / 8);
+    a.tb = cache_tokens_per_cta(a.tokens);
+    a.claims = nullptr;
+    a.w = 1;
+    switch (y_dtype) {
+        case GPTQ_BF16: return cache_read_fmt<__nv_bfloat16>(a, format, s);
+        case GPTQ_F16: return cache_read_fmt<__half>(a, format, s);
+        default: return cache_read_fmt<float>(a, format, s);
+    }
+}
+
+}  // namespace serve
+}  // namespace gptq

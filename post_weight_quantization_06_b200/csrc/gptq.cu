@@ -13,6 +13,9 @@
 #include "gptq2d.cuh"
 #include "hessian_tc.cuh"
 #include "lll.cuh"
+#include "fp8_quant.cuh"
+#include "fp8_mm.cuh"
+#include "cache.cuh"
 
 namespace gptq {
 
@@ -792,6 +795,182 @@ GPTQ_API int gptq_quantize_layer_reduced(const void *W, int w_dtype, int64_t m, 
                                          void *workspace, size_t ws_bytes, gptq_stream_t stream) {
     const int st = gptq_quantize_layer_reduced_body(W, w_dtype, m, n, H, bits, lambda_rel, codes,
         scales, zeros, loss_out, coef_out, stats_out, workspace, ws_bytes, stream);
+    return finish_call(st, stream);
+}
+
+// ---------------------------------------------------------------------------------------
+// gptq_serve.h
+// ---------------------------------------------------------------------------------------
+static int gptq_fp8_quantize_body(const void *X, int x_dtype, int64_t rows, int64_t cols,
+                                  int64_t ldx, int block_rows, void *codes, int64_t ldc,
+                                  float *scales, gptq_stream_t stream) {
+    if (!serve::serve_dtype_ok(x_dtype) || (block_rows != 1 && block_rows != 128)) return GPTQ_ERR_ARG;
+    if (rows < 0 || cols < 0 || cols > 0x7fffffffLL || rows > 0x7fffffffLL) return GPTQ_ERR_ARG;
+    if (rows == 0 || cols == 0) return GPTQ_OK;
+    if (!X || !codes || !scales || ldx < cols || ldc < cols) return GPTQ_ERR_ARG;
+    if (rows * ((cols + 127) / 128) > 0x7fffffffLL) return GPTQ_ERR_ARG;
+    return serve::fp8_quantize(X, x_dtype, rows, cols, ldx, block_rows, codes, ldc, scales,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+GPTQ_API int gptq_fp8_quantize(const void *X, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               int block_rows, void *codes, int64_t ldc, float *scales,
+                               gptq_stream_t stream) {
+    const int st = gptq_fp8_quantize_body(X, x_dtype, rows, cols, ldx, block_rows, codes, ldc, scales,
+                                          stream);
+    return finish_call(st, stream);
+}
+
+static int gptq_fp8_matmul_body(const void *A, int64_t lda, const float *sA, const void *B,
+                                int64_t ldb, const float *sB, int64_t m, int64_t n, int64_t k,
+                                void *Y, int y_dtype, int64_t ldy, gptq_stream_t stream) {
+    const int64_t most = 0x7fffffffLL - 256;
+    if (!serve::serve_dtype_ok(y_dtype)) return GPTQ_ERR_ARG;
+    if (m < 0 || n < 0 || k < 0 || m > most || n > most || k > most) return GPTQ_ERR_ARG;
+    if (m == 0 || n == 0) return GPTQ_OK;
+    if (!Y || ldy < n) return GPTQ_ERR_ARG;
+    if (k > 0) {
+        // the pitch of a single row is of no account
+        if (m == 1) lda = (k + 15) / 16 * 16;
+        if (n == 1) ldb = (k + 15) / 16 * 16;
+        if (!A || !B || !sA || !sB || lda < k || ldb < k || lda % 16 || ldb % 16) return GPTQ_ERR_ARG;
+        if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) & 15u) return GPTQ_ERR_ARG;
+    }
+    return serve::fp8_matmul(A, lda, sA, B, ldb, sB, m, n, k, Y, y_dtype, ldy,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+GPTQ_API int gptq_fp8_matmul(const void *A, int64_t lda, const float *sA, const void *B,
+                             int64_t ldb, const float *sB, int64_t m, int64_t n, int64_t k,
+                             void *Y, int y_dtype, int64_t ldy, gptq_stream_t stream) {
+    const int st = gptq_fp8_matmul_body(A, lda, sA, B, ldb, sB, m, n, k, Y, y_dtype, ldy, stream);
+    return finish_call(st, stream);
+}
+
+// Checks what both cache calls share and fills the arguments that do not depend on the values.
+static int cache_check(serve::CacheArgs &a, const int64_t *slots, int64_t tokens, int64_t n_slots,
+                       int heads, int head_dim, int format, int group_size, const void *codes_k,
+                       const float *scales_k, const uint8_t *zeros_k, const void *codes_v,
+                       const float *scales_v, const uint8_t *zeros_v, bool two) {
+    if (format != GPTQ_CACHE_INT4 && format != GPTQ_CACHE_INT8 && format != GPTQ_CACHE_E4M3)
+        return GPTQ_ERR_ARG;
+    if (tokens < 0 || tokens > 0x7fffffffLL - 256 || n_slots < 0 || heads < 1 || head_dim < 8 ||
+        head_dim % 8 || group_size < 0)
+        return GPTQ_ERR_ARG;
+    const int group = group_size ? group_size : head_dim;
+    if (group % 8 || group > 1024 || head_dim % group) return GPTQ_ERR_ARG;
+    if ((int64_t)heads * head_dim > serve::CACHE_MAX_HD) return GPTQ_ERR_ARG;
+    if (tokens == 0) return GPTQ_OK;
+    const bool grid = format != GPTQ_CACHE_E4M3;
+    if (!slots || !codes_k || !scales_k || (grid && !zeros_k)) return GPTQ_ERR_ARG;
+    if (two && (!codes_v || !scales_v || (grid && !zeros_v))) return GPTQ_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(codes_k) | (two ? reinterpret_cast<uintptr_t>(codes_v) : 0)) & 7u)
+        return GPTQ_ERR_ARG;
+    a.slots = slots;
+    a.n_slots = n_slots;
+    a.tokens = (int)tokens;
+    a.heads = heads;
+    a.dim = head_dim;
+    a.group = group;
+    a.claims = nullptr;
+    for (int i = 0; i < 2; ++i) {
+        serve::CachePlane &p = a.p[i];
+        const bool v = i == 1;
+        p.x = p.y = nullptr;
+        p.codes = static_cast<unsigned char *>(const_cast<void *>(v ? codes_v : codes_k));
+        p.scales = const_cast<float *>(v ? scales_v : scales_k);
+        p.zeros = const_cast<uint8_t *>(v ? zeros_v : zeros_k);
+        p.ts = p.hs = 0;
+        p.vec = 0;
+    }
+    return GPTQ_OK;
+}
+// Whether the heads of all tokens lie apart from one another (what is written has to).
+static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+    if (tokens == 1) return heads == 1 || hs >= dim;
+    if (heads == 1) return ts >= dim;
+    return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
+}
+static int cache_vec(const void *x, int64_t ts, int64_t hs, int dtype) {
+    const int64_t per = 16 / serve::serve_dtype_bytes(dtype);
+    return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ts % per == 0 && hs % per == 0;
+}
+
+static int gptq_cache_write_body(const void *K, int64_t k_token_stride, int64_t k_head_stride,
+                                 const void *V, int64_t v_token_stride, int64_t v_head_stride,
+                                 int x_dtype, int64_t tokens, int heads, int head_dim,
+                                 const int64_t *slots, int64_t n_slots, int format, int group_size,
+                                 void *codes_k, float *scales_k, uint8_t *zeros_k, void *codes_v,
+                                 float *scales_v, uint8_t *zeros_v, int32_t *claims,
+                                 gptq_stream_t stream) {
+    serve::CacheArgs a;
+    if (!serve::serve_dtype_ok(x_dtype)) return GPTQ_ERR_ARG;
+    if (int st = cache_check(a, slots, tokens, n_slots, heads, head_dim, format, group_size, codes_k,
+                             scales_k, zeros_k, codes_v, scales_v, zeros_v, V != nullptr))
+        return st;
+    if (tokens == 0) return GPTQ_OK;
+    if (!K || (tokens > GPTQ_CACHE_UNCLAIMED && !claims)) return GPTQ_ERR_ARG;
+    a.claims = claims;
+    a.p[0].x = K;
+    a.p[0].ts = k_token_stride;
+    a.p[0].hs = k_head_stride;
+    a.p[0].vec = cache_vec(K, k_token_stride, k_head_stride, x_dtype);
+    a.p[1].x = V;
+    a.p[1].ts = v_token_stride;
+    a.p[1].hs = v_head_stride;
+    a.p[1].vec = cache_vec(V, v_token_stride, v_head_stride, x_dtype);
+    return serve::cache_write(a, x_dtype, format, reinterpret_cast<cudaStream_t>(stream));
+}
+
+GPTQ_API int gptq_cache_write(const void *K, int64_t k_token_stride, int64_t k_head_stride,
+                              const void *V, int64_t v_token_stride, int64_t v_head_stride,
+                              int x_dtype, int64_t tokens, int heads, int head_dim,
+                              const int64_t *slots, int64_t n_slots, int format, int group_size,
+                              void *codes_k, float *scales_k, uint8_t *zeros_k, void *codes_v,
+                              float *scales_v, uint8_t *zeros_v, int32_t *claims,
+                              gptq_stream_t stream) {
+    const int st = gptq_cache_write_body(K, k_token_stride, k_head_stride, V, v_token_stride,
+        v_head_stride, x_dtype, tokens, heads, head_dim, slots, n_slots, format, group_size, codes_k,
+        scales_k, zeros_k, codes_v, scales_v, zeros_v, claims, stream);
+    return finish_call(st, stream);
+}
+
+static int gptq_cache_read_body(const int64_t *slots, int64_t tokens, int64_t n_slots, int heads,
+                                int head_dim, int format, int group_size, const void *codes_k,
+                                const float *scales_k, const uint8_t *zeros_k, const void *codes_v,
+                                const float *scales_v, const uint8_t *zeros_v, void *K,
+                                int64_t k_token_stride, int64_t k_head_stride, void *V,
+                                int64_t v_token_stride, int64_t v_head_stride, int y_dtype,
+                                gptq_stream_t stream) {
+    serve::CacheArgs a;
+    if (!serve::serve_dtype_ok(y_dtype)) return GPTQ_ERR_ARG;
+    if (int st = cache_check(a, slots, tokens, n_slots, heads, head_dim, format, group_size, codes_k,
+                             scales_k, zeros_k, codes_v, scales_v, zeros_v, V != nullptr))
+        return st;
+    if (tokens == 0) return GPTQ_OK;
+    if (!K || !rows_apart(tokens, heads, head_dim, k_token_stride, k_head_stride)) return GPTQ_ERR_ARG;
+    if (V && !rows_apart(tokens, heads, head_dim, v_token_stride, v_head_stride)) return GPTQ_ERR_ARG;
+    a.p[0].y = K;
+    a.p[0].ts = k_token_stride;
+    a.p[0].hs = k_head_stride;
+    a.p[0].vec = cache_vec(K, k_token_stride, k_head_stride, y_dtype);
+    a.p[1].y = V;
+    a.p[1].ts = v_token_stride;
+    a.p[1].hs = v_head_stride;
+    a.p[1].vec = cache_vec(V, v_token_stride, v_head_stride, y_dtype);
+    return serve::cache_read(a, y_dtype, format, reinterpret_cast<cudaStream_t>(stream));
+}
+
+GPTQ_API int gptq_cache_read(const int64_t *slots, int64_t tokens, int64_t n_slots, int heads,
+                             int head_dim, int format, int group_size, const void *codes_k,
+                             const float *scales_k, const uint8_t *zeros_k, const void *codes_v,
+                             const float *scales_v, const uint8_t *zeros_v, void *K,
+                             int64_t k_token_stride, int64_t k_head_stride, void *V,
+                             int64_t v_token_stride, int64_t v_head_stride, int y_dtype,
+                             gptq_stream_t stream) {
+    const int st = gptq_cache_read_body(slots, tokens, n_slots, heads, head_dim, format, group_size,
+        codes_k, scales_k, zeros_k, codes_v, scales_v, zeros_v, K, k_token_stride, k_head_stride, V,
+        v_token_stride, v_head_stride, y_dtype, stream);
     return finish_call(st, stream);
 }
 

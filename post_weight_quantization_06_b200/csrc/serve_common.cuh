@@ -1,0 +1,130 @@
+// Shared pieces of the serving operators (8-bit block product, quantized cache): vectors of eight
+// values of the three input types, the conversion to e4m3, division by a number fixed per call.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "gptq_serve.h"
+
+namespace gptq {
+namespace serve {
+
+constexpr float E4M3_MAX = 448.f;
+constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126: a scale and its reciprocal stay normal
+constexpr uint32_t INF_BITS = 0x7f800000u;
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T narrow(float x);
+template <> __device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
+
+// Eight values as they lie in memory: one 16-byte word of a 16-bit type, two of fp32.
+template <typename T>
+struct Raw8 {
+    static constexpr int WORDS = 8 * sizeof(T) / 16;
+    uint4 w[WORDS];
+};
+
+// `vec`: all eight are there and p is 16-byte aligned. Otherwise the first `have` (0..8) are
+// loaded one by one and the others are zero. (Plain loads throughout: these kernels may start while
+// the one before them still writes, which the read-only path does not allow.)
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, int have, Raw8<T> &r) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < Raw8<T>::WORDS; ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    } else {
+        T *e = reinterpret_cast<T *>(r.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < have ? p[i] : narrow<T>(0.f);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T> &r, float *v) {
+    const T *e = reinterpret_cast<const T *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = widen(e[i]);
+}
+// Eight fp32 values rounded to T and stored.
+template <typename T>
+__device__ __forceinline__ void store8(T *p, bool vec, const float *v) {
+    Raw8<T> r;
+    T *e = reinterpret_cast<T *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = narrow<T>(v[i]);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < Raw8<T>::WORDS; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = e[i];
+    }
+}
+
+// Largest |v| as fp32 bits: these order like the values, NaN above infinity above the rest, so
+// one maximum also tells whether all eight are finite.
+__device__ __forceinline__ uint32_t amax_bits8(const float *v) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+    return a;
+}
+// The finite ones' largest; the others become NaN. Rare.
+__device__ __forceinline__ uint32_t amax_finite8(float *v) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+        if (b >= INF_BITS) v[i] = __uint_as_float(0x7fffffffu);
+        else a = max(a, b);
+    }
+    return a;
+}
+
+__device__ __forceinline__ float e4m3_scale(uint32_t amax) {
+    return fmaxf(__fdiv_rn(__uint_as_float(amax), E4M3_MAX), SCALE_MIN);
+}
+
+// x r truncated to fp32 with the last bit set where the truncation dropped something: rounding
+// that to e4m3 rounds the exact product (a nearest product could itself land on a border
+// between two codes, which would then be decided by the even one).
+__device__ __forceinline__ float mul_sticky(float x, float r) {
+    const float p = __fmul_rz(x, r);
+    const float d = __fmaf_rn(x, r, -p);
+    return d != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+// Eight e4m3 codes of v under the reciprocal scale r, the first in the lowest byte.
+__device__ __forceinline__ uint2 e4m3_codes8(const float *v, float r) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = e4m3_pair(mul_sticky(v[2 * i], r), mul_sticky(v[2 * i + 1], r));
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// n / d by a multiplication, exact for n * d < 2^32 (the error of the rounded-up reciprocal,
+// below d / 2^32 per unit of n, then never reaches the next whole number).
+struct FastDiv {
+    uint32_t d, m;
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return m ? __umulhi(n, m) : n; }
+};
+inline FastDiv fast_div(uint32_t d) {
+    return FastDiv{d, d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u};
+}
+
+inline bool serve_dtype_ok(int t) { return t == GPTQ_BF16 || t == GPTQ_F32 || t == GPTQ_F16; }
+inline int serve_dtype_bytes(int t) { return t == GPTQ_F32 ? 4 : 2; }
+
+}  // namespace serve
+}  // namespace gptq
