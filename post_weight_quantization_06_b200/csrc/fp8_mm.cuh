@@ -7,6 +7,8 @@
 // "promotion" warps while the next block's MMAs run into another accumulator.
 #pragma once
 
+#include <algorithm>
+
 #include "hessian_tc.cuh"
 #include "serve_common.cuh"
 
@@ -17,7 +19,6 @@ using tc::cluster_sync_all;
 using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;
-using tc::mbar_wait;
 using tc::mma_commit;
 using tc::smem_u32;
 using tc::tc_fence_after;
@@ -51,6 +52,56 @@ __device__ __forceinline__ void mma_e4m3(uint32_t dtmem, uint64_t adesc, uint64_
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
+// One lane of a converged warp. The producer's and the issuer's loops are run by whole warps, with
+// this lane alone issuing: under `lane == 0` the compiler cannot keep descriptors and addresses
+// in uniform registers, and an iteration of four MMAs took 900 cycles.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ bool mm_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits for the phase with this parity. False, with the abort flag set, if `limit` cycles pass
+// first (recorded with `site`) or another role gave up.
+__device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, long long limit,
+                                        volatile int *abort_flag, int site) {
+    const uint32_t addr = smem_u32(bar);
+    if (mm_try(addr, parity)) return true;
+    const long long t0 = clock64();
+    while (!mm_try(addr, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            report(GPTQ_ERR_TIMEOUT, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// After an abort: copies in flight land within microseconds, before the shared memory goes away.
+__device__ __forceinline__ void mm_drain() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) { }
+}
+// Position in a ring of N with the parity of its current round.
+template <int N>
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) { i = 0; phase ^= 1u; }
+    }
+};
 // 16 columns of this thread's TMEM lane, without the wait; mm_wait_ld16 ties the wait to them.
 __device__ __forceinline__ void mm_ld16(uint32_t taddr, uint32_t *r) {
     asm volatile(
@@ -76,10 +127,56 @@ __device__ __forceinline__ void cp_async4(void *dst, const void *src, bool on) {
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+                 "f"(c), "f"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// acc (two fp32) += t * s, both halves
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t t0, uint32_t t1, uint64_t s2) {
+    asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(t0), "r"(t1), "l"(s2));
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
     return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t *r) {
+    mm_ld16(taddr, r);
+    mm_ld16(taddr + 16, r + 16);
+}
+__device__ __forceinline__ void mm_wait_ld32(uint32_t *r) {
+    mm_wait_ld16(r);
+    mm_wait_ld16(r + 16);
+}
+// Four values of a row of Y, columns col .. col + 3 of n.
+template <typename TY>
+__device__ __forceinline__ void store_y4(TY *y, int col, int n, bool vec, float4 v) {
+    const TY t[4] = {narrow<TY>(v.x), narrow<TY>(v.y), narrow<TY>(v.z), narrow<TY>(v.w)};
+    if (vec && col + 4 <= n) {
+        if (sizeof(TY) == 4) *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(t);
+        else *reinterpret_cast<uint2 *>(y) = *reinterpret_cast<const uint2 *>(t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < n) y[i] = t[i];
+    }
 }
 
 struct MmArgs {
@@ -87,15 +184,20 @@ struct MmArgs {
     void *Y;
     long long ldy;
     int m, n, kb;            // kb: blocks of K
-    int tiles_n;             // 128-row tiles of B
+    int nb128;               // blocks of 128 columns of Y
+    int tiles_m, tiles_n;
     int split;               // CTAs of a cluster, each with a part of the K blocks
+    int rows;                // narrow kernel: rows of B of a CTA, 64 or 128
+    int vec;                 // four values of Y can be stored at once
     long long wait_limit;
 };
 
 // ---------------------------------------------------------------------------------------
 // Few rows of A (decode): the weights' rows are the MMA's 128 rows and NT tokens its columns, so
-// a 128 x NT tile costs only the weight's bytes. The blocks of K are split over the `split` CTAs of a
-// cluster, which add their sums through distributed shared memory in a fixed order.
+// a tile costs only the weight's bytes. The blocks of K are split over the `split` CTAs of a
+// cluster; each sends its sums to the CTA that owns the token, which adds them in the order of
+// the parts. A CTA that has only 64 rows of the weight leaves the other half of the operand as
+// it is: the rows of the product do not mix, and that half of the accumulator is not read.
 //
 // Warps: 0 TMA, 1 TMEM and MMA, 2-5 promotion (32 weight rows each), 6 scales.
 // ---------------------------------------------------------------------------------------
@@ -104,18 +206,17 @@ constexpr int NARROW_THREADS = 224;
 template <int NT>
 struct NarrowShape {
     static constexpr int W_BYTES = 128 * MM_BK;
-    static constexpr int X_BYTES = NT * MM_BK;
-    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int STAGES = NT <= 32 ? 9 : NT <= 64 ? 8 : 6;
+    static constexpr int STAGE_BYTES = W_BYTES + NT * MM_BK;
+    static constexpr int STAGES = NT <= 16 ? 10 : NT <= 32 ? 8 : 6;
     static constexpr int SLOT = NT + 4;   // scales of NT tokens, then the weight tile's
-    static constexpr int BUFS = NT <= 64 ? 4 : 2;
-    static constexpr int TMEM = NT * BUFS < 32 ? 32 : NT * BUFS;
-    static constexpr int BARS = 2 * STAGES + 2 * BUFS + 2 * MM_SCALE_SLOTS + 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES +
+    static constexpr int BUFS = 4;
+    static constexpr int TMEM = NT * BUFS;
+    static constexpr int BARS = 2 * STAGES + 2 * BUFS + 2 * MM_SCALE_SLOTS + 1;
+    static constexpr int RED = (NT + 7) * 128;   // floats received from the cluster
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + sizeof(float) * RED +
                                    sizeof(float) * MM_SCALE_SLOTS * SLOT + 8 * BARS + 64;
     static_assert(SMEM <= 232448, "fits the shared memory of one CTA");
-    static_assert((TMEM & (TMEM - 1)) == 0 && TMEM <= 512, "a TMEM allocation");
-    static_assert(NT * 128 * 4 <= STAGES * STAGE_BYTES, "partial sums fit the stages");
+    static_assert((TMEM & (TMEM - 1)) == 0 && TMEM >= 32 && TMEM <= 512, "a TMEM allocation");
 };
 
 template <int NT, typename TY>
@@ -126,7 +227,8 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     extern __shared__ __align__(1024) unsigned char mm_smem[];
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
-    float *scale_ring = reinterpret_cast<float *>(stages + S::STAGES * S::STAGE_BYTES);
+    float *red = reinterpret_cast<float *>(stages + S::STAGES * S::STAGE_BYTES);
+    float *scale_ring = red + S::RED;
     uint64_t *full = reinterpret_cast<uint64_t *>(scale_ring + MM_SCALE_SLOTS * S::SLOT);
     uint64_t *empty = full + S::STAGES;
     uint64_t *acc_full = empty + S::STAGES;
@@ -141,25 +243,31 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     const int part = a.split > 1 ? (int)tc::cluster_rank() : 0;
     const int tile = (int)(blockIdx.x / (unsigned)a.split);
     const int tn = tile % a.tiles_n, tm = tile / a.tiles_n;
-    const int n0 = tn * 128, m0 = tm * NT;
+    const int n0 = tn * a.rows, m0 = tm * NT;
     const int b0 = (int)((long long)a.kb * part / a.split);
     const int nb = (int)((long long)a.kb * (part + 1) / a.split) - b0;  // this CTA's blocks
+    const int quarters = a.rows >> 5;   // promotion warps with rows
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < S::BUFS; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
-        for (int i = 0; i < MM_SCALE_SLOTS; ++i) { mbar_init(&s_full[i], 32); mbar_init(&s_empty[i], 4); }
-        mbar_init(mma_done, 1);
-        *abort_flag = 0;
+    if (warp == 0) {
+        for (int i = lane; i < S::BARS; i += 32) {
+            uint64_t *b = full + i;
+            const uint32_t count = (b >= acc_empty && b < s_full) || (b >= s_empty && b < mma_done)
+                                       ? (uint32_t)quarters
+                                       : (b >= s_full && b < s_empty) ? 32u : 1u;
+            mbar_init(b, count);
+        }
+        if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 1) {
+        __syncwarp();
+    } else if (warp == 1) {
         tmem_alloc(tmem_slot, S::TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // the CTAs of a cluster have to be there before one writes to another (waited for below)
+    if (a.split > 1) cluster_arrive();
     const uint32_t tmem = *tmem_slot;
     // the next kernel may start its own set-up now: this CTA holds its TMEM already
     pdl_launch_next();
@@ -170,81 +278,73 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     for (int j = 0; j < NT; ++j) acc[j] = 0.f;
 
     if (warp == 0) {
-        if (lane == 0) {
-            for (int it = 0; it < nb; ++it) {
-                const int st = it % S::STAGES;
-                if (*abort_flag) break;
-                if (!mbar_wait(&empty[st], (uint32_t)((it / S::STAGES) & 1) ^ 1u, a.wait_limit)) {
-                    report(GPTQ_ERR_TIMEOUT, 11);
-                    *abort_flag = 1;
-                    break;
-                }
-                unsigned char *w = stages + st * S::STAGE_BYTES;
-                mbar_expect_tx(&full[st], S::STAGE_BYTES);
-                tma_load_2d(&wmap, &full[st], w, (b0 + it) * MM_BK, n0);
-                tma_load_2d(&xmap, &full[st], w + S::W_BYTES, (b0 + it) * MM_BK, m0);
+        const bool one = elect_one();
+        const uint32_t bytes = (uint32_t)(a.rows + NT) * MM_BK;
+        Ring<S::STAGES> st;
+        bool ok = true;
+        for (int it = 0; it < nb; ++it, st.next()) {
+            ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 11);
+            if (!ok) break;
+            if (one) {
+                unsigned char *w = stages + st.i * S::STAGE_BYTES;
+                mbar_expect_tx(&full[st.i], bytes);
+                tma_load_2d(&wmap, &full[st.i], w, (b0 + it) * MM_BK, n0);
+                tma_load_2d(&xmap, &full[st.i], w + S::W_BYTES, (b0 + it) * MM_BK, m0);
             }
-            if (*abort_flag) {
-                // copies in flight land within microseconds: before the shared memory goes away
-                const long long t0 = clock64();
-                while (clock64() - t0 < 2000000) { }
-            }
+            __syncwarp();
         }
+        if (!ok) mm_drain();
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int it = 0; it < nb && !*abort_flag; ++it) {
-                const int b = it % S::BUFS, st = it % S::STAGES;
-                if (!mbar_wait(&acc_empty[b], (uint32_t)((it / S::BUFS) & 1) ^ 1u, a.wait_limit) ||
-                    !mbar_wait(&full[st], (uint32_t)((it / S::STAGES) & 1), a.wait_limit)) {
-                    report(GPTQ_ERR_TIMEOUT, 12);
-                    *abort_flag = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t w = smem_u32(stages + st * S::STAGE_BYTES);
-#pragma unroll
-                for (int k = 0; k < MM_BK / 32; ++k)
-                    mma_e4m3(tmem + (uint32_t)(b * NT), mm_desc(w + 32 * k),
-                             mm_desc(w + S::W_BYTES + 32 * k), mm_idesc(128, NT), k > 0);
-                mma_commit(&empty[st]);
-                mma_commit(&acc_full[b]);
-            }
-            mma_commit(mma_done);
-            mbar_wait(mma_done, 0, a.wait_limit);
-        }
-    } else if (warp == 6) {
-        for (int it = 0; it < nb && !*abort_flag; ++it) {
-            const int sl = it % MM_SCALE_SLOTS;
-            if (!mbar_wait(&s_empty[sl], (uint32_t)((it / MM_SCALE_SLOTS) & 1) ^ 1u, a.wait_limit)) {
-                if (lane == 0) report(GPTQ_ERR_TIMEOUT, 13);
-                *abort_flag = 1;
+        const bool one = elect_one();
+        Ring<S::STAGES> st;
+        Ring<S::BUFS> b;
+        for (int it = 0; it < nb; ++it, st.next(), b.next()) {
+            if (!mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 12) ||
+                !mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 13))
                 break;
+            tc_fence_after();
+            if (one) {
+                const uint32_t w = smem_u32(stages + st.i * S::STAGE_BYTES);
+                const uint64_t wd = mm_desc(w), xd = mm_desc(w + S::W_BYTES);
+#pragma unroll
+                for (int k = 0; k < MM_BK / 32; ++k)   // 32 codes: 32 bytes further, in units of 16
+                    mma_e4m3(tmem + (uint32_t)(b.i * NT), wd + 2 * k, xd + 2 * k, mm_idesc(128, NT),
+                             k > 0);
+                mma_commit(&empty[st.i]);
+                mma_commit(&acc_full[b.i]);
             }
-            float *d = scale_ring + sl * S::SLOT;
+            __syncwarp();
+        }
+        if (one) mma_commit(mma_done);
+        mm_wait(mma_done, 0, a.wait_limit, abort_flag, 14);
+    } else if (warp == 6) {
+        Ring<MM_SCALE_SLOTS> sl;
+        const float *sw = a.sB + (long long)(n0 >> 7) * a.kb + b0;
+        for (int it = 0; it < nb; ++it, sl.next()) {
+            if (!mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 15)) break;
+            float *d = scale_ring + sl.i * S::SLOT;
 #pragma unroll
             for (int j = lane; j < NT; j += 32) {
                 const bool on = m0 + j < a.m;
                 cp_async4(d + j, a.sA + (on ? (long long)(m0 + j) * a.kb + b0 + it : 0), on);
             }
-            if (lane == 0) cp_async4(d + NT, a.sB + (long long)tn * a.kb + b0 + it, true);
-            cp_async_arrive(&s_full[sl]);
+            if (lane == 0) cp_async4(d + NT, sw + it, true);
+            cp_async_arrive(&s_full[sl.i]);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
+    } else if ((warp & 3) < quarters) {
         const int q = warp & 3;
-        for (int it = 0; it < nb && !*abort_flag; ++it) {
-            const int b = it % S::BUFS, sl = it % MM_SCALE_SLOTS;
-            if (!mbar_wait(&s_full[sl], (uint32_t)((it / MM_SCALE_SLOTS) & 1), a.wait_limit) ||
-                !mbar_wait(&acc_full[b], (uint32_t)((it / S::BUFS) & 1), a.wait_limit)) {
-                if (lane == 0) report(GPTQ_ERR_TIMEOUT, 14);
-                *abort_flag = 1;
+        Ring<MM_SCALE_SLOTS> sl;
+        Ring<S::BUFS> b;
+        for (int it = 0; it < nb; ++it, sl.next(), b.next()) {
+            if (!mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 16) ||
+                !mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 17))
                 break;
-            }
             __syncwarp();
             tc_fence_after();
-            const float *d = scale_ring + sl * S::SLOT;
+            const float *d = scale_ring + sl.i * S::SLOT;
             const float sw = d[NT];
-            const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * NT);
+            const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b.i * NT);
 #pragma unroll
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
@@ -261,45 +361,486 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) { mbar_arrive(&acc_empty[b]); mbar_arrive(&s_empty[sl]); }
+            if (lane == 0) { mbar_arrive(&acc_empty[b.i]); mbar_arrive(&s_empty[sl.i]); }
+        }
+    }
+    __syncwarp();
+
+    const bool adds = warp >= 2 && warp < 6 && (warp & 3) < quarters;
+    const int row = 32 * (warp & 3) + lane;  // of the weight tile
+    const int mt = a.m - m0 < NT ? a.m - m0 : NT;
+    TY *Y = static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0;
+    if (a.split == 1) {
+        if (adds && n0 + row < a.n) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (j < mt) Y[(long long)j * a.ldy + row] = narrow<TY>(acc[j]);
+        }
+    } else {
+        const int own = (NT + a.split - 1) / a.split;   // tokens of a CTA, at most
+        cluster_wait();
+        if (adds) {
+            int dst = 0, at = part * own;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (j < mt) st_cluster(tc::map_to_rank(red + at * 128 + row, (uint32_t)dst), acc[j]);
+                if (++dst == a.split) { dst = 0; ++at; }
+            }
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        // token part + split * l, the parts in order
+        for (int i = threadIdx.x; i < own * 128; i += NARROW_THREADS) {
+            const int j = part + a.split * (i >> 7), r = i & 127;
+            if (j >= mt || r >= a.rows || n0 + r >= a.n) continue;
+            float t = red[i];
+            for (int p = 1; p < a.split; ++p) t += red[p * own * 128 + i];
+            Y[(long long)j * a.ldy + r] = narrow<TY>(t);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, S::TMEM);
+}
 
-    const bool adds = warp >= 2 && warp < 6;
-    const int row = 32 * (warp & 3) + lane;  // of the weight tile
-    TY *Y = static_cast<TY *>(a.Y);
-    if (a.split == 1) {
-        if (adds && n0 + row < a.n) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (m0 + j < a.m) Y[(long long)(m0 + j) * a.ldy + n0 + row] = narrow<TY>(acc[j]);
+// ---------------------------------------------------------------------------------------
+// More rows of A than a decode batch, too few tiles for the pair kernel: 128 x 128 tiles of Y,
+// one CTA each, the rows of A on the TMEM lanes, so that a promotion thread has one row and its
+// scale is one number per block. The blocks of K can be split over a cluster as above.
+//
+// Warps: 0 TMA, 1 TMEM and MMA, 2 scales, 4-11 promotion (32 rows x 64 columns each).
+// ---------------------------------------------------------------------------------------
+constexpr int TILE_THREADS = 384;
+constexpr int TILE_STAGES = 6;
+constexpr int TILE_STAGE_BYTES = 2 * 128 * MM_BK;
+constexpr int TILE_BUFS = 4;
+constexpr int TILE_SLOT = 128 + 4;
+constexpr int TILE_BARS = 2 * TILE_STAGES + 2 * TILE_BUFS + 2 * MM_SCALE_SLOTS + 1;
+constexpr int TILE_PITCH = 132;   // floats of a row of sums in shared memory: no bank conflicts
+constexpr size_t TILE_SMEM = 1024 + (size_t)TILE_STAGES * TILE_STAGE_BYTES +
+                             sizeof(float) * MM_SCALE_SLOTS * TILE_SLOT + 8 * TILE_BARS + 64;
+static_assert(TILE_SMEM <= 232448, "fits the shared memory of one CTA");
+static_assert((128 + 7) * TILE_PITCH * 4 <= TILE_STAGES * TILE_STAGE_BYTES, "sums fit the stages");
+
+template <typename TY>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ MmArgs a) {
+    extern __shared__ __align__(1024) unsigned char mm_smem[];
+    unsigned char *stages = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
+    float *scale_ring = reinterpret_cast<float *>(stages + TILE_STAGES * TILE_STAGE_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(scale_ring + MM_SCALE_SLOTS * TILE_SLOT);
+    uint64_t *empty = full + TILE_STAGES;
+    uint64_t *acc_full = empty + TILE_STAGES;
+    uint64_t *acc_empty = acc_full + TILE_BUFS;
+    uint64_t *s_full = acc_empty + TILE_BUFS;
+    uint64_t *s_empty = s_full + MM_SCALE_SLOTS;
+    uint64_t *mma_done = s_empty + MM_SCALE_SLOTS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = a.split > 1 ? (int)tc::cluster_rank() : 0;
+    const int tile = (int)(blockIdx.x / (unsigned)a.split);
+    const int tn = tile % a.tiles_n, tm = tile / a.tiles_n;
+    const int n0 = tn * 128, m0 = tm * 128;
+    const int b0 = (int)((long long)a.kb * part / a.split);
+    const int nb = (int)((long long)a.kb * (part + 1) / a.split) - b0;
+
+    if (warp == 0) {
+        for (int i = lane; i < TILE_BARS; i += 32) {
+            uint64_t *b = full + i;
+            const uint32_t count = (b >= acc_empty && b < s_full) || (b >= s_empty && b < mma_done)
+                                       ? 8u : (b >= s_full && b < s_empty) ? 32u : 1u;
+            mbar_init(b, count);
         }
-        return;
+        if (lane == 0) *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+    } else if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
     }
-    // the stages are free: every copy was waited for and every MMA is done
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_next();
+    pdl_wait_prev();
+
+    uint64_t acc[32];   // 64 columns of one row, in pairs
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = 0;
+
+    if (warp == 0) {
+        const bool one = elect_one();
+        Ring<TILE_STAGES> st;
+        bool ok = true;
+        for (int it = 0; it < nb; ++it, st.next()) {
+            ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 21);
+            if (!ok) break;
+            if (one) {
+                unsigned char *sa = stages + st.i * TILE_STAGE_BYTES;
+                mbar_expect_tx(&full[st.i], TILE_STAGE_BYTES);
+                tma_load_2d(&amap, &full[st.i], sa, (b0 + it) * MM_BK, m0);
+                tma_load_2d(&bmap, &full[st.i], sa + 128 * MM_BK, (b0 + it) * MM_BK, n0);
+            }
+            __syncwarp();
+        }
+        if (!ok) mm_drain();
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        Ring<TILE_STAGES> st;
+        Ring<TILE_BUFS> b;
+        for (int it = 0; it < nb; ++it, st.next(), b.next()) {
+            if (!mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 22) ||
+                !mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 23))
+                break;
+            tc_fence_after();
+            if (one) {
+                const uint32_t w = smem_u32(stages + st.i * TILE_STAGE_BYTES);
+                const uint64_t ad = mm_desc(w), bd = mm_desc(w + 128 * MM_BK);
+#pragma unroll
+                for (int k = 0; k < MM_BK / 32; ++k)
+                    mma_e4m3(tmem + (uint32_t)(b.i * 128), ad + 2 * k, bd + 2 * k,
+                             mm_idesc(128, 128), k > 0);
+                mma_commit(&empty[st.i]);
+                mma_commit(&acc_full[b.i]);
+            }
+            __syncwarp();
+        }
+        if (one) mma_commit(mma_done);
+        mm_wait(mma_done, 0, a.wait_limit, abort_flag, 24);
+    } else if (warp == 2) {
+        Ring<MM_SCALE_SLOTS> sl;
+        for (int it = 0; it < nb; ++it, sl.next()) {
+            if (!mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 25)) break;
+            float *d = scale_ring + sl.i * TILE_SLOT;
+#pragma unroll
+            for (int j = lane; j < 128; j += 32) {
+                const bool on = m0 + j < a.m;
+                cp_async4(d + j, a.sA + (on ? (long long)(m0 + j) * a.kb + b0 + it : 0), on);
+            }
+            if (lane == 0) cp_async4(d + 128, a.sB + (long long)tn * a.kb + b0 + it, true);
+            cp_async_arrive(&s_full[sl.i]);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= 4) {
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        Ring<MM_SCALE_SLOTS> sl;
+        Ring<TILE_BUFS> b;
+        for (int it = 0; it < nb; ++it, sl.next(), b.next()) {
+            if (!mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 26) ||
+                !mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 27))
+                break;
+            __syncwarp();
+            tc_fence_after();
+            const float *d = scale_ring + sl.i * TILE_SLOT;
+            const float s = d[32 * q + lane] * d[128];
+            const uint64_t s2 = pair_of(s, s);
+            const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b.i * 128 + 64 * h);
+            uint32_t r0[32], r1[32];
+            mm_ld32(t, r0);
+            mm_ld32(t + 32, r1);
+            mm_wait_ld32(r0);
+            mm_wait_ld32(r1);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) { mbar_arrive(&acc_empty[b.i]); mbar_arrive(&s_empty[sl.i]); }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[j], r0[2 * j], r0[2 * j + 1], s2);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[16 + j], r1[2 * j], r1[2 * j + 1], s2);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+
+    // Sums by row through shared memory (the stages are free: every copy was waited for and every
+    // MMA is done), then whole rows to Y. Row i belongs to CTA i % split of the cluster.
     float *sum = reinterpret_cast<float *>(stages);
-    if (adds) {
+    const int own = (128 + a.split - 1) / a.split;
+    if (a.split > 1) cluster_sync_all();
+    if (warp >= 4) {
+        const int i = 32 * (warp & 3) + lane, h = (warp - 4) >> 2;
+        float *d = sum + ((long long)part * own + i / a.split) * TILE_PITCH + 64 * h;
+        if (a.split > 1) {
+            const uint32_t to = tc::map_to_rank(d, (uint32_t)(i % a.split));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) sum[j * 128 + row] = acc[j];
+            for (int j = 0; j < 32; j += 2) {
+                const float2 u = unpair(acc[j]), v = unpair(acc[j + 1]);
+                st_cluster4(to + 8 * j, u.x, u.y, v.x, v.y);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float2 u = unpair(acc[j]), v = unpair(acc[j + 1]);
+                *reinterpret_cast<float4 *>(d + 2 * j) = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
     }
-    cluster_sync_all();
-    for (int i = part * NARROW_THREADS + (int)threadIdx.x; i < NT * 128; i += a.split * NARROW_THREADS) {
-        const int j = i >> 7, r = i & 127;
-        float v[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            v[p] = p < a.split ? ld_cluster_f32(tc::map_to_rank(sum + i, (uint32_t)p)) : 0.f;
-        float t = v[0];
-#pragma unroll
-        for (int p = 1; p < 8; ++p)
-            if (p < a.split) t += v[p];
-        if (m0 + j < a.m && n0 + r < a.n) Y[(long long)(m0 + j) * a.ldy + n0 + r] = narrow<TY>(t);
+    if (a.split > 1) cluster_sync_all();
+    else __syncthreads();
+    const int col = n0 + 4 * lane;
+    for (int l = warp; l < own; l += TILE_THREADS / 32) {
+        const int i = part + a.split * l;
+        if (i >= 128 || m0 + i >= a.m || col >= a.n) continue;
+        const float *d = sum + (long long)l * TILE_PITCH + 4 * lane;
+        float4 v = *reinterpret_cast<const float4 *>(d);
+        for (int p = 1; p < a.split; ++p) {
+            const float4 w = *reinterpret_cast<const float4 *>(d + (long long)p * own * TILE_PITCH);
+            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+        }
+        store_y4(static_cast<TY *>(a.Y) + (long long)(m0 + i) * a.ldy + col, col, a.n, a.vec, v);
     }
-    cluster_sync_all();  // no CTA leaves while another still reads its sums
+}
+
+// ---------------------------------------------------------------------------------------
+// Many rows: 256 x 256 tiles of Y by a CTA pair (tcgen05 cta_group::2), persistent. CTA r holds
+// rows 128 r .. of the pair's A and B; the leader's 256 x 256 x 32 MMAs read both CTAs' shared
+// memory and leave rows 128 r .. of the tile in CTA r's TMEM. A block of K takes the tensor cores
+// 512 cycles; in that time a promotion thread reads 128 columns of its row from one of two
+// accumulators and adds them, in pairs, to 128 sums in registers (setmaxnreg: 232 for the
+// promotion warps, 40 for the others, together the 168 x 384 of the launch).
+//
+// Warps: 0 TMA, 1 TMEM and (leader) MMA, 2 scales, 4-11 promotion (32 rows x 128 columns each).
+// ---------------------------------------------------------------------------------------
+constexpr int PAIR_THREADS = 384;
+constexpr int PAIR_STAGES = 5;
+constexpr int PAIR_STAGE_BYTES = 2 * 128 * MM_BK;   // this CTA's halves of A and B
+constexpr int PAIR_SLOT = 128 + 4;
+constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 2 * MM_SCALE_SLOTS + 1;
+constexpr int PAIR_PITCH = 36;                      // floats of a row of an output slice
+constexpr int PAIR_OUT = 8 * 32 * PAIR_PITCH;       // a 32 x 32 slice per promotion warp
+constexpr size_t PAIR_SMEM = 1024 + (size_t)PAIR_STAGES * PAIR_STAGE_BYTES + sizeof(float) * PAIR_OUT +
+                             sizeof(float) * MM_SCALE_SLOTS * PAIR_SLOT + 8 * PAIR_BARS + 64;
+static_assert(PAIR_SMEM <= 232448, "fits the shared memory of one CTA");
+constexpr int PAIR_GROUP = 8;   // tile rows that are walked together, column by column
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
+        "l"(adesc), "l"(bdesc), "r"(mm_idesc(256, 256)), "r"(accumulate));
+}
+// Tile t in groups of PAIR_GROUP tile rows, so that the tiles in flight share rows and columns
+// that the L2 holds.
+__device__ __forceinline__ void pair_tile(const MmArgs &a, int t, int &tm, int &tn) {
+    const int per = PAIR_GROUP * a.tiles_n, g = t / per, r = t - g * per;
+    const int h = min(PAIR_GROUP, a.tiles_m - g * PAIR_GROUP);
+    tn = r / h;
+    tm = g * PAIR_GROUP + (r - tn * h);
+}
+
+template <typename TY>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ MmArgs a) {
+    extern __shared__ __align__(1024) unsigned char mm_smem[];
+    unsigned char *stages = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
+    float *out = reinterpret_cast<float *>(stages + PAIR_STAGES * PAIR_STAGE_BYTES);
+    float *scale_ring = out + PAIR_OUT;
+    uint64_t *full = reinterpret_cast<uint64_t *>(scale_ring + MM_SCALE_SLOTS * PAIR_SLOT);  // leader's
+    uint64_t *empty = full + PAIR_STAGES;
+    uint64_t *acc_full = empty + PAIR_STAGES;   // 2
+    uint64_t *acc_empty = acc_full + 2;         // 2, the leader's
+    uint64_t *s_full = acc_empty + 2;
+    uint64_t *s_empty = s_full + MM_SCALE_SLOTS;
+    uint64_t *mma_done = s_empty + MM_SCALE_SLOTS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int tiles = a.tiles_m * a.tiles_n;
+
+    if (warp == 0) {
+        for (int i = lane; i < PAIR_BARS; i += 32) {
+            uint64_t *b = full + i;
+            const uint32_t count = b >= acc_empty && b < s_full ? 16u
+                                   : b >= s_empty && b < mma_done ? 8u
+                                   : b >= s_full && b < s_empty ? 32u : 1u;
+            mbar_init(b, count);
+        }
+        if (lane == 0) *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+    } else if (warp == 1) {
+        tc::tmem_alloc_pair(tmem_slot, 512);
+        tc::tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive or TMA
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_next();
+    pdl_wait_prev();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            const bool one = elect_one();
+            Ring<PAIR_STAGES> st;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += npairs) {
+                int tm, tn;
+                pair_tile(a, t, tm, tn);
+                const int ya = tm * 256 + 128 * (int)rank, yb = tn * 256 + 128 * (int)rank;
+                for (int kb = 0; kb < a.kb; ++kb, st.next()) {
+                    ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 31);
+                    if (!ok) break;
+                    if (one) {
+                        unsigned char *sa = stages + st.i * PAIR_STAGE_BYTES;
+                        // the leader's barrier counts both CTAs' bytes
+                        if (rank == 0) mbar_expect_tx(&full[st.i], 2 * PAIR_STAGE_BYTES);
+                        const uint32_t fb = tc::map_to_rank(&full[st.i], 0);
+                        tc::tma_load_2d_pair(&amap, fb, sa, kb * MM_BK, ya);
+                        tc::tma_load_2d_pair(&bmap, fb, sa + 128 * MM_BK, kb * MM_BK, yb);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) mm_drain();
+        } else if (warp == 1) {
+            if (rank == 0) {
+                const bool one = elect_one();
+                Ring<PAIR_STAGES> st;
+                Ring<2> b;
+                bool ok = true;
+                for (int t = pair; t < tiles && ok; t += npairs) {
+                    for (int kb = 0; kb < a.kb; ++kb, st.next(), b.next()) {
+                        ok = mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 32) &&
+                             mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 33);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (one) {
+                            const uint32_t w = smem_u32(stages + st.i * PAIR_STAGE_BYTES);
+                            const uint64_t ad = mm_desc(w), bd = mm_desc(w + 128 * MM_BK);
+#pragma unroll
+                            for (int k = 0; k < MM_BK / 32; ++k)
+                                mma_e4m3_pair(tmem + (uint32_t)(b.i * 256), ad + 2 * k, bd + 2 * k, k > 0);
+                            tc::mma_commit_pair(&empty[st.i], 0x3);
+                            tc::mma_commit_pair(&acc_full[b.i], 0x3);
+                        }
+                        __syncwarp();
+                    }
+                }
+                // all MMAs complete before the pair's TMEM is released
+                if (one) tc::mma_commit_pair(mma_done, 0x1);
+                mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
+            }
+        } else if (warp == 2) {
+            Ring<MM_SCALE_SLOTS> sl;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += npairs) {
+                int tm, tn;
+                pair_tile(a, t, tm, tn);
+                const int m0 = tm * 256 + 128 * (int)rank;
+                const bool two = 2 * tn + lane < a.nb128;   // lanes 0 and 1: the tile's column blocks
+                const float *sb = a.sB + (two ? (long long)(2 * tn + lane) * a.kb : 0);
+                for (int kb = 0; kb < a.kb; ++kb, sl.next()) {
+                    ok = mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 35);
+                    if (!ok) break;
+                    float *d = scale_ring + sl.i * PAIR_SLOT;
+#pragma unroll
+                    for (int j = lane; j < 128; j += 32) {
+                        const bool on = m0 + j < a.m;
+                        cp_async4(d + j, a.sA + (on ? (long long)(m0 + j) * a.kb + kb : 0), on);
+                    }
+                    if (lane < 2) cp_async4(d + 128 + lane, sb + (two ? kb : 0), two);
+                    cp_async_arrive(&s_full[sl.i]);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const uint32_t te0 = tc::map_to_rank(&acc_empty[0], 0), te1 = tc::map_to_rank(&acc_empty[1], 0);
+        float *slice = out + (warp - 4) * 32 * PAIR_PITCH;
+        Ring<MM_SCALE_SLOTS> sl;
+        Ring<2> b;
+        bool ok = true;
+        for (int t = pair; t < tiles; t += npairs) {
+            uint64_t acc[64];   // 128 columns of one row, in pairs
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int kb = 0; kb < a.kb; ++kb, sl.next(), b.next()) {
+                ok = mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 36) &&
+                     mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 37);
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+                const float *d = scale_ring + sl.i * PAIR_SLOT;
+                const float s = d[32 * q + lane] * d[128 + h];
+                const uint64_t s2 = pair_of(s, s);
+                const uint32_t tt = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b.i * 256 + 128 * h);
+                uint32_t r0[32], r1[32];
+                mm_ld32(tt, r0);
+                mm_wait_ld32(r0);
+                mm_ld32(tt + 32, r1);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[j], r0[2 * j], r0[2 * j + 1], s2);
+                mm_wait_ld32(r1);
+                mm_ld32(tt + 64, r0);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[16 + j], r1[2 * j], r1[2 * j + 1], s2);
+                mm_wait_ld32(r0);
+                mm_ld32(tt + 96, r1);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[32 + j], r0[2 * j], r0[2 * j + 1], s2);
+                mm_wait_ld32(r1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive_remote(b.i ? te1 : te0);
+                    mbar_arrive(&s_empty[sl.i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[48 + j], r1[2 * j], r1[2 * j + 1], s2);
+            }
+            if (!ok) break;
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
+            // 32 columns at a time through shared memory: rows of the slice leave as whole sectors
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (n0 + 32 * c >= a.n || m0 >= a.m) continue;   // the same in the whole warp
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float2 u = unpair(acc[16 * c + j]), v = unpair(acc[16 * c + j + 1]);
+                    *reinterpret_cast<float4 *>(slice + lane * PAIR_PITCH + 2 * j) =
+                        make_float4(u.x, u.y, v.x, v.y);
+                }
+                __syncwarp();
+                const int col = n0 + 32 * c + 4 * (lane & 7);
+#pragma unroll
+                for (int r = lane >> 3; r < 32; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(slice + r * PAIR_PITCH + 4 * (lane & 7));
+                    if (m0 + r < a.m && col < a.n)
+                        store_y4(static_cast<TY *>(a.Y) + (long long)(m0 + r) * a.ldy + col, col, a.n,
+                                 a.vec, v);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the peer's TMEM, barriers and shared memory outlive every access
+    tc_fence_after();
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -318,39 +859,101 @@ inline bool mm_map(CUtensorMap *map, const void *p, long long rows, long long k,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, typename TY>
-inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb, long long k,
-                     MmArgs a, cudaStream_t s) {
-    using S = NarrowShape<NT>;
-    CUtensorMap wmap, xmap;
-    if (!mm_map(&wmap, B, a.n, k, ldb, 128) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
-    auto kernel = fp8_mm_narrow_kernel<NT, TY>;
-    GPTQ_SMEM_LIMIT(kernel, S::SMEM);
-    a.tiles_n = ceil_div(a.n, 128);
-    const long long tiles = (long long)a.tiles_n * ceil_div(a.m, NT);
-    // as many parts of K as fill the SMs, at most a portable cluster's eight
-    long long split = device_sm_count() / tiles;
-    if (split > 8) split = 8;
-    if (split > a.kb) split = a.kb;
-    if (split < 1) split = 1;
-    a.split = (int)split;
-    if (tiles * split > 0x7fffffffLL) return GPTQ_ERR_ARG;
+template <typename K>
+inline int mm_launch(K kernel, long long ctas, int cluster, int threads, size_t smem,
+                     const CUtensorMap &x, const CUtensorMap &y, const MmArgs &a, cudaStream_t s) {
+    if (ctas > 0x7fffffffLL) return GPTQ_ERR_ARG;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(NARROW_THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, x, y, a);
     const int st = launch_status();
     return e == cudaSuccess ? st : GPTQ_ERR_CUDA;
+}
+
+// CTAs with an SM's shared memory that run at once in clusters of `size`, from the occupancy
+// call on a B200 of 148 SMs, whose clusters do not cross the borders of its SM groups: larger
+// clusters leave SMs idle (seven: 105).
+inline int mm_resident(int size) {
+    static const int on148[9] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
+    const int sms = device_sm_count();
+    return sms >= 148 ? on148[size] : sms / size * size * 3 / 4;
+}
+// Parts of K for `tiles` tiles: the fewest blocks on the critical path, rounds of CTAs x blocks of
+// a CTA, with `extra` blocks' time for the reduction.
+inline int mm_split(long long tiles, int kb, int extra, long long &cost) {
+    int best = 1;
+    cost = -1;
+    for (int s = 1; s <= 8 && s <= kb; ++s) {
+        const int at_once = mm_resident(s) / s * s;
+        if (at_once < s) continue;
+        const long long rounds = (tiles * s + at_once - 1) / at_once;
+        const long long c = rounds * ((kb + s - 1) / s + extra + (s > 1 ? extra : 0));
+        if (cost < 0 || c < cost) { cost = c; best = s; }
+    }
+    return best;
+}
+
+template <int NT, typename TY>
+inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb, long long k,
+                     MmArgs a, cudaStream_t s) {
+    using S = NarrowShape<NT>;
+    a.tiles_m = ceil_div(a.m, NT);
+    // 64 rows a CTA where that leaves fewer bytes on the critical path: half the bytes a block
+    long long c128, c64;
+    const int s128 = mm_split((long long)ceil_div(a.n, 128) * a.tiles_m, a.kb, 4, c128);
+    const int s64 = mm_split((long long)ceil_div(a.n, 64) * a.tiles_m, a.kb, 6, c64);
+    const bool half = 2 * c64 < 3 * c128 && a.n > 64;
+    a.rows = half ? 64 : 128;
+    a.split = half ? s64 : s128;
+    a.tiles_n = ceil_div(a.n, a.rows);
+    CUtensorMap wmap, xmap;
+    if (!mm_map(&wmap, B, a.n, k, ldb, a.rows) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
+    auto kernel = fp8_mm_narrow_kernel<NT, TY>;
+    GPTQ_SMEM_LIMIT(kernel, S::SMEM);
+    return mm_launch(kernel, (long long)a.tiles_n * a.tiles_m * a.split, a.split, NARROW_THREADS, S::SMEM,
+                     wmap, xmap, a, s);
+}
+
+template <typename TY>
+inline int mm_tile(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
+                   cudaStream_t s) {
+    a.tiles_m = ceil_div(a.m, 128);
+    a.tiles_n = ceil_div(a.n, 128);
+    long long cost;
+    a.split = mm_split((long long)a.tiles_m * a.tiles_n, a.kb, 4, cost);
+    CUtensorMap amap, bmap;
+    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
+    auto kernel = fp8_mm_tile_kernel<TY>;
+    GPTQ_SMEM_LIMIT(kernel, TILE_SMEM);
+    return mm_launch(kernel, (long long)a.tiles_m * a.tiles_n * a.split, a.split, TILE_THREADS, TILE_SMEM,
+                     amap, bmap, a, s);
+}
+
+template <typename TY>
+inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
+                   cudaStream_t s) {
+    a.tiles_m = ceil_div(a.m, 256);
+    a.tiles_n = ceil_div(a.n, 256);
+    const long long tiles = (long long)a.tiles_m * a.tiles_n;
+    if (tiles > 0x7fffffffLL - 1024) return GPTQ_ERR_ARG;
+    a.split = 1;
+    CUtensorMap amap, bmap;
+    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
+    auto kernel = fp8_mm_pair_kernel<TY>;
+    GPTQ_SMEM_LIMIT(kernel, PAIR_SMEM);
+    const long long pairs = std::min<long long>(tiles, device_sm_count() / 2);
+    return mm_launch(kernel, 2 * pairs, 2, PAIR_THREADS, PAIR_SMEM, amap, bmap, a, s);
 }
 
 template <typename TY>
@@ -359,18 +962,19 @@ inline int mm_type(const void *A, long long lda, const void *B, long long ldb, l
     if (a.m <= 16) return mm_narrow<16, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 32) return mm_narrow<32, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 64) return mm_narrow<64, TY>(A, lda, B, ldb, k, a, s);
-    return mm_narrow<128, TY>(A, lda, B, ldb, k, a, s);
+    const long long pair_tiles = (long long)ceil_div(a.m, 256) * ceil_div(a.n, 256);
+    if (pair_tiles >= device_sm_count() / 2) return mm_pair<TY>(A, lda, B, ldb, k, a, s);
+    return mm_tile<TY>(A, lda, B, ldb, k, a, s);
 }
 
 inline int fp8_matmul(const void *A, long long lda, const float *sA, const void *B, long long ldb,
                       const float *sB, long long m, long long n, long long k, void *Y, int y_dtype,
                       long long ldy, cudaStream_t s) {
-    if (k == 0) {
-        const size_t b = (size_t)serve_dtype_bytes(y_dtype);
-        return cudaMemset2DAsync(Y, (size_t)ldy * b, 0, (size_t)n * b, (size_t)m, s) == cudaSuccess
+    const int size = serve_dtype_bytes(y_dtype);
+    if (k == 0)
+        return cudaMemset2DAsync(Y, (size_t)ldy * size, 0, (size_t)n * size, (size_t)m, s) == cudaSuccess
                    ? GPTQ_OK : GPTQ_ERR_CUDA;
-    }
-    MmArgs a;
+    MmArgs a = {};
     a.sA = sA;
     a.sB = sB;
     a.Y = Y;
@@ -378,7 +982,8 @@ inline int fp8_matmul(const void *A, long long lda, const float *sA, const void 
     a.m = (int)m;
     a.n = (int)n;
     a.kb = (int)((k + MM_BK - 1) / MM_BK);
-    a.tiles_n = a.split = 0;
+    a.nb128 = ceil_div(n, 128);
+    a.vec = ldy % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % (4 * size) == 0;
     // a wait longer than ~2 s at the 1.9 GHz clock means a lost signal, not a slow kernel
     a.wait_limit = tc::env_ll("GPTQ_WAIT_LIMIT_CYCLES", 4000000000LL);
     switch (y_dtype) {
