@@ -88,6 +88,12 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, long lon
     }
     return true;
 }
+// Arrival on a barrier of the pair's leader. What it orders are TMEM loads that have completed
+// (tcgen05.wait::ld), so the default scope will do: a release at cluster scope fences the thread's
+// memory first and cost the promotion a thousand cycles a block.
+__device__ __forceinline__ void mm_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // After an abort: copies in flight land within microseconds, before the shared memory goes away.
 __device__ __forceinline__ void mm_drain() {
     const long long t0 = clock64();
@@ -606,19 +612,19 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 // memory and leave rows 128 r .. of the tile in CTA r's TMEM. A block of K takes the tensor cores
 // 512 cycles; in that time a promotion thread reads 128 columns of its row from one of two
 // accumulators and adds them, in pairs, to 128 sums in registers (setmaxnreg: 232 for the
-// promotion warps, 40 for the others, together the 168 x 384 of the launch).
+// promotion warps, 40 for the others, together the 168 x 384 of the launch). Its row's scales come
+// straight from memory, four blocks at a time and a group ahead.
 //
-// Warps: 0 TMA, 1 TMEM and (leader) MMA, 2 scales, 4-11 promotion (32 rows x 128 columns each).
+// Warps: 0 TMA, 1 TMEM and (leader) MMA, 4-11 promotion (32 rows x 128 columns each).
 // ---------------------------------------------------------------------------------------
 constexpr int PAIR_THREADS = 384;
 constexpr int PAIR_STAGES = 5;
 constexpr int PAIR_STAGE_BYTES = 2 * 128 * MM_BK;   // this CTA's halves of A and B
-constexpr int PAIR_SLOT = 128 + 4;
-constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 2 * MM_SCALE_SLOTS + 1;
+constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 1;
 constexpr int PAIR_PITCH = 36;                      // floats of a row of an output slice
 constexpr int PAIR_OUT = 8 * 32 * PAIR_PITCH;       // a 32 x 32 slice per promotion warp
 constexpr size_t PAIR_SMEM = 1024 + (size_t)PAIR_STAGES * PAIR_STAGE_BYTES + sizeof(float) * PAIR_OUT +
-                             sizeof(float) * MM_SCALE_SLOTS * PAIR_SLOT + 8 * PAIR_BARS + 64;
+                             8 * PAIR_BARS + 64;
 static_assert(PAIR_SMEM <= 232448, "fits the shared memory of one CTA");
 constexpr int PAIR_GROUP = 8;   // tile rows that are walked together, column by column
 
@@ -638,6 +644,28 @@ __device__ __forceinline__ void pair_tile(const MmArgs &a, int t, int &tm, int &
     tm = g * PAIR_GROUP + (r - tn * h);
 }
 
+// The two scales of blocks kb .. kb + 3 (those that are there). The product is taken a group of
+// blocks later: taken here it would wait for the loads.
+struct Scales4 {
+    float4 x, y;
+    __device__ __forceinline__ void load(const float *pa, const float *pb, int kb, int nkb, bool vec) {
+        if (vec) {
+            if (kb < nkb) {
+                x = *reinterpret_cast<const float4 *>(pa + kb);
+                y = *reinterpret_cast<const float4 *>(pb + kb);
+            }
+        } else {
+            if (kb < nkb) { x.x = pa[kb]; y.x = pb[kb]; }
+            if (kb + 1 < nkb) { x.y = pa[kb + 1]; y.y = pb[kb + 1]; }
+            if (kb + 2 < nkb) { x.z = pa[kb + 2]; y.z = pb[kb + 2]; }
+            if (kb + 3 < nkb) { x.w = pa[kb + 3]; y.w = pb[kb + 3]; }
+        }
+    }
+    __device__ __forceinline__ float4 product() const {
+        return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+    }
+};
+
 template <typename TY>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
@@ -646,14 +674,11 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
     float *out = reinterpret_cast<float *>(stages + PAIR_STAGES * PAIR_STAGE_BYTES);
-    float *scale_ring = out + PAIR_OUT;
-    uint64_t *full = reinterpret_cast<uint64_t *>(scale_ring + MM_SCALE_SLOTS * PAIR_SLOT);  // leader's
+    uint64_t *full = reinterpret_cast<uint64_t *>(out + PAIR_OUT);   // the leader's
     uint64_t *empty = full + PAIR_STAGES;
     uint64_t *acc_full = empty + PAIR_STAGES;   // 2
     uint64_t *acc_empty = acc_full + 2;         // 2, the leader's
-    uint64_t *s_full = acc_empty + 2;
-    uint64_t *s_empty = s_full + MM_SCALE_SLOTS;
-    uint64_t *mma_done = s_empty + MM_SCALE_SLOTS;
+    uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -665,10 +690,7 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (warp == 0) {
         for (int i = lane; i < PAIR_BARS; i += 32) {
             uint64_t *b = full + i;
-            const uint32_t count = b >= acc_empty && b < s_full ? 16u
-                                   : b >= s_empty && b < mma_done ? 8u
-                                   : b >= s_full && b < s_empty ? 32u : 1u;
-            mbar_init(b, count);
+            mbar_init(b, b >= acc_empty && b < mma_done ? 16u : 1u);
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -738,29 +760,6 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                 if (one) tc::mma_commit_pair(mma_done, 0x1);
                 mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
             }
-        } else if (warp == 2) {
-            Ring<MM_SCALE_SLOTS> sl;
-            bool ok = true;
-            for (int t = pair; t < tiles && ok; t += npairs) {
-                int tm, tn;
-                pair_tile(a, t, tm, tn);
-                const int m0 = tm * 256 + 128 * (int)rank;
-                const bool two = 2 * tn + lane < a.nb128;   // lanes 0 and 1: the tile's column blocks
-                const float *sb = a.sB + (two ? (long long)(2 * tn + lane) * a.kb : 0);
-                for (int kb = 0; kb < a.kb; ++kb, sl.next()) {
-                    ok = mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 35);
-                    if (!ok) break;
-                    float *d = scale_ring + sl.i * PAIR_SLOT;
-#pragma unroll
-                    for (int j = lane; j < 128; j += 32) {
-                        const bool on = m0 + j < a.m;
-                        cp_async4(d + j, a.sA + (on ? (long long)(m0 + j) * a.kb + kb : 0), on);
-                    }
-                    if (lane < 2) cp_async4(d + 128 + lane, sb + (two ? kb : 0), two);
-                    cp_async_arrive(&s_full[sl.i]);
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -768,21 +767,34 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t te0 = tc::map_to_rank(&acc_empty[0], 0), te1 = tc::map_to_rank(&acc_empty[1], 0);
         float *slice = out + (warp - 4) * 32 * PAIR_PITCH;
-        Ring<MM_SCALE_SLOTS> sl;
         Ring<2> b;
         bool ok = true;
+        const bool vec = (a.kb & 3) == 0 &&
+                         ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15u) == 0;
         for (int t = pair; t < tiles; t += npairs) {
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
+            // rows and columns behind the last take its scales: what they scale is not stored
+            const float *pa = a.sA + (long long)min(m0 + lane, a.m - 1) * a.kb;
+            const float *pb = a.sB + (long long)min(2 * tn + h, a.nb128 - 1) * a.kb;
+            Scales4 next = {};
+            next.load(pa, pb, 0, a.kb, vec);
+            float4 sc = {};
             uint64_t acc[64];   // 128 columns of one row, in pairs
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
-            for (int kb = 0; kb < a.kb; ++kb, sl.next(), b.next()) {
-                ok = mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 36) &&
-                     mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 37);
+            for (int kb = 0; kb < a.kb; ++kb, b.next()) {
+                if ((kb & 3) == 0) {
+                    sc = next.product();
+                    next.load(pa, pb, kb + 4, a.kb, vec);
+                }
+                const float s = sc.x;
+                sc.x = sc.y; sc.y = sc.z; sc.z = sc.w;
+                ok = mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 37);
                 if (!ok) break;
                 __syncwarp();
                 tc_fence_after();
-                const float *d = scale_ring + sl.i * PAIR_SLOT;
-                const float s = d[32 * q + lane] * d[128 + h];
                 const uint64_t s2 = pair_of(s, s);
                 const uint32_t tt = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b.i * 256 + 128 * h);
                 uint32_t r0[32], r1[32];
@@ -802,17 +814,11 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                 mm_wait_ld32(r1);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive_remote(b.i ? te1 : te0);
-                    mbar_arrive(&s_empty[sl.i]);
-                }
+                if (lane == 0) mm_arrive_remote(b.i ? te1 : te0);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) fma2(acc[48 + j], r1[2 * j], r1[2 * j + 1], s2);
             }
             if (!ok) break;
-            int tm, tn;
-            pair_tile(a, t, tm, tn);
-            const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
             // 32 columns at a time through shared memory: rows of the slice leave as whole sectors
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
