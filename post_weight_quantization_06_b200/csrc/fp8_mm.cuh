@@ -88,12 +88,6 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, long lon
     }
     return true;
 }
-// Arrival on a barrier of the pair's leader. What it orders are TMEM loads that have completed
-// (tcgen05.wait::ld), so the default scope will do: a release at cluster scope fences the thread's
-// memory first and cost the promotion a thousand cycles a block.
-__device__ __forceinline__ void mm_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 // After an abort: copies in flight land within microseconds, before the shared memory goes away.
 __device__ __forceinline__ void mm_drain() {
     const long long t0 = clock64();
@@ -164,18 +158,31 @@ __device__ __forceinline__ float2 unpair(uint64_t v) {
     return f;
 }
 __device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t *r) {
-    mm_ld16(taddr, r);
-    mm_ld16(taddr + 16, r + 16);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                 "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+                 "}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                       "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                       "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                       "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ void mm_wait_ld32(uint32_t *r) {
-    mm_wait_ld16(r);
-    mm_wait_ld16(r + 16);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]),
+          "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+          "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+          "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+          "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+          "+r"(r[31])::"memory");
 }
-// Four values of a row of Y, columns col .. col + 3 of n.
+// Four values of a row of Y from column col on, those before n.
 template <typename TY>
-__device__ __forceinline__ void store_y4(TY *y, int col, int n, bool vec, float4 v) {
+__device__ __forceinline__ void store_y4(TY *y, int col, int n, float4 v) {
     const TY t[4] = {narrow<TY>(v.x), narrow<TY>(v.y), narrow<TY>(v.z), narrow<TY>(v.w)};
-    if (vec && col + 4 <= n) {
+    if (col + 4 <= n) {
         if (sizeof(TY) == 4) *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(t);
         else *reinterpret_cast<uint2 *>(y) = *reinterpret_cast<const uint2 *>(t);
     } else {
@@ -184,7 +191,6 @@ __device__ __forceinline__ void store_y4(TY *y, int col, int n, bool vec, float4
             if (col + i < n) y[i] = t[i];
     }
 }
-
 struct MmArgs {
     const float *sA, *sB;
     void *Y;
@@ -193,8 +199,7 @@ struct MmArgs {
     int nb128;               // blocks of 128 columns of Y
     int tiles_m, tiles_n;
     int split;               // CTAs of a cluster, each with a part of the K blocks
-    int rows;                // narrow kernel: rows of B of a CTA, 64 or 128
-    int vec;                 // four values of Y can be stored at once
+    int vec, vec16;          // four values, or 16 bytes, of Y can be stored at once
     long long wait_limit;
 };
 
@@ -202,8 +207,7 @@ struct MmArgs {
 // Few rows of A (decode): the weights' rows are the MMA's 128 rows and NT tokens its columns, so
 // a tile costs only the weight's bytes. The blocks of K are split over the `split` CTAs of a
 // cluster; each sends its sums to the CTA that owns the token, which adds them in the order of
-// the parts. A CTA that has only 64 rows of the weight leaves the other half of the operand as
-// it is: the rows of the product do not mix, and that half of the accumulator is not read.
+// the parts. (64 rows a CTA, to split less, took as long or longer at every size tried.)
 //
 // Warps: 0 TMA, 1 TMEM and MMA, 2-5 promotion (32 weight rows each), 6 scales.
 // ---------------------------------------------------------------------------------------
@@ -213,7 +217,7 @@ template <int NT>
 struct NarrowShape {
     static constexpr int W_BYTES = 128 * MM_BK;
     static constexpr int STAGE_BYTES = W_BYTES + NT * MM_BK;
-    static constexpr int STAGES = NT <= 16 ? 10 : NT <= 32 ? 8 : 6;
+    static constexpr int STAGES = NT <= 16 ? 10 : 8;
     static constexpr int SLOT = NT + 4;   // scales of NT tokens, then the weight tile's
     static constexpr int BUFS = 4;
     static constexpr int TMEM = NT * BUFS;
@@ -249,16 +253,15 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     const int part = a.split > 1 ? (int)tc::cluster_rank() : 0;
     const int tile = (int)(blockIdx.x / (unsigned)a.split);
     const int tn = tile % a.tiles_n, tm = tile / a.tiles_n;
-    const int n0 = tn * a.rows, m0 = tm * NT;
+    const int n0 = tn * 128, m0 = tm * NT;
     const int b0 = (int)((long long)a.kb * part / a.split);
     const int nb = (int)((long long)a.kb * (part + 1) / a.split) - b0;  // this CTA's blocks
-    const int quarters = a.rows >> 5;   // promotion warps with rows
 
     if (warp == 0) {
         for (int i = lane; i < S::BARS; i += 32) {
             uint64_t *b = full + i;
             const uint32_t count = (b >= acc_empty && b < s_full) || (b >= s_empty && b < mma_done)
-                                       ? (uint32_t)quarters
+                                       ? 4u
                                        : (b >= s_full && b < s_empty) ? 32u : 1u;
             mbar_init(b, count);
         }
@@ -285,7 +288,6 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
 
     if (warp == 0) {
         const bool one = elect_one();
-        const uint32_t bytes = (uint32_t)(a.rows + NT) * MM_BK;
         Ring<S::STAGES> st;
         bool ok = true;
         for (int it = 0; it < nb; ++it, st.next()) {
@@ -293,7 +295,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             if (!ok) break;
             if (one) {
                 unsigned char *w = stages + st.i * S::STAGE_BYTES;
-                mbar_expect_tx(&full[st.i], bytes);
+                mbar_expect_tx(&full[st.i], S::STAGE_BYTES);
                 tma_load_2d(&wmap, &full[st.i], w, (b0 + it) * MM_BK, n0);
                 tma_load_2d(&xmap, &full[st.i], w + S::W_BYTES, (b0 + it) * MM_BK, m0);
             }
@@ -325,7 +327,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
         mm_wait(mma_done, 0, a.wait_limit, abort_flag, 14);
     } else if (warp == 6) {
         Ring<MM_SCALE_SLOTS> sl;
-        const float *sw = a.sB + (long long)(n0 >> 7) * a.kb + b0;
+        const float *sw = a.sB + (long long)tn * a.kb + b0;
         for (int it = 0; it < nb; ++it, sl.next()) {
             if (!mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 15)) break;
             float *d = scale_ring + sl.i * S::SLOT;
@@ -338,7 +340,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             cp_async_arrive(&s_full[sl.i]);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if ((warp & 3) < quarters) {
+    } else {
         const int q = warp & 3;
         Ring<MM_SCALE_SLOTS> sl;
         Ring<S::BUFS> b;
@@ -372,7 +374,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     }
     __syncwarp();
 
-    const bool adds = warp >= 2 && warp < 6 && (warp & 3) < quarters;
+    const bool adds = warp >= 2 && warp < 6;
     const int row = 32 * (warp & 3) + lane;  // of the weight tile
     const int mt = a.m - m0 < NT ? a.m - m0 : NT;
     TY *Y = static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0;
@@ -399,7 +401,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
         // token part + split * l, the parts in order
         for (int i = threadIdx.x; i < own * 128; i += NARROW_THREADS) {
             const int j = part + a.split * (i >> 7), r = i & 127;
-            if (j >= mt || r >= a.rows || n0 + r >= a.n) continue;
+            if (j >= mt || n0 + r >= a.n) continue;
             float t = red[i];
             for (int p = 1; p < a.split; ++p) t += red[p * own * 128 + i];
             Y[(long long)j * a.ldy + r] = narrow<TY>(t);
@@ -592,56 +594,61 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     if (a.split > 1) cluster_sync_all();
     else __syncthreads();
-    const int col = n0 + 4 * lane;
     for (int l = warp; l < own; l += TILE_THREADS / 32) {
         const int i = part + a.split * l;
-        if (i >= 128 || m0 + i >= a.m || col >= a.n) continue;
-        const float *d = sum + (long long)l * TILE_PITCH + 4 * lane;
-        float4 v = *reinterpret_cast<const float4 *>(d);
-        for (int p = 1; p < a.split; ++p) {
-            const float4 w = *reinterpret_cast<const float4 *>(d + (long long)p * own * TILE_PITCH);
-            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+        if (i >= 128 || m0 + i >= a.m) continue;
+        const float *d = sum + (long long)l * TILE_PITCH;
+        TY *y = static_cast<TY *>(a.Y) + (long long)(m0 + i) * a.ldy + n0;
+        if (a.vec) {   // four columns a lane
+            const int c = 4 * lane;
+            float4 v = *reinterpret_cast<const float4 *>(d + c);
+            for (int p = 1; p < a.split; ++p) {
+                const float4 w = *reinterpret_cast<const float4 *>(d + (long long)p * own * TILE_PITCH + c);
+                v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+            }
+            store_y4(y + c, n0 + c, a.n, v);
+        } else {       // rows that are not aligned: neighbouring lanes store neighbouring columns
+#pragma unroll
+            for (int c = lane; c < 128; c += 32) {
+                float v = d[c];
+                for (int p = 1; p < a.split; ++p) v += d[(long long)p * own * TILE_PITCH + c];
+                if (n0 + c < a.n) y[c] = narrow<TY>(v);
+            }
         }
-        store_y4(static_cast<TY *>(a.Y) + (long long)(m0 + i) * a.ldy + col, col, a.n, a.vec, v);
     }
 }
 
 // ---------------------------------------------------------------------------------------
-// Many rows: 256 x 256 tiles of Y by a CTA pair (tcgen05 cta_group::2), persistent. CTA r holds
-// rows 128 r .. of the pair's A and B; the leader's 256 x 256 x 32 MMAs read both CTAs' shared
-// memory and leave rows 128 r .. of the tile in CTA r's TMEM. A block of K takes the tensor cores
-// 512 cycles; in that time a promotion thread reads 128 columns of its row from one of two
-// accumulators and adds them, in pairs, to 128 sums in registers (setmaxnreg: 232 for the
-// promotion warps, 40 for the others, together the 168 x 384 of the launch). Its row's scales come
-// straight from memory, four blocks at a time and a group ahead.
+// Many rows: 128 x 256 tiles of Y, persistent, one CTA per SM. A block of K takes the tensor cores
+// 512 cycles (four 128 x 256 x 32 MMAs into one of two accumulators); in that time a promotion
+// thread reads the 128 columns of its row from the other one and adds them to 128 sums in
+// registers (setmaxnreg: 232 for the promotion warps, 40 for the others, together the 168 x 384
+// of the launch). Its row's scales come straight from memory, four blocks at a time and a group
+// ahead. With two accumulators what counts is the way from a block's last MMA to the release of
+// its accumulator: a CTA pair (cta_group::2), which moves two thirds of the bytes, takes 930 cycles
+// a block, since commits and arrivals cross to the other SM; this one takes 820.
 //
-// Warps: 0 TMA, 1 TMEM and (leader) MMA, 4-11 promotion (32 rows x 128 columns each).
+// Warps: 0 TMA, 1 TMEM and MMA, 4-11 promotion (32 rows x 128 columns each).
 // ---------------------------------------------------------------------------------------
-constexpr int PAIR_THREADS = 384;
-constexpr int PAIR_STAGES = 5;
-constexpr int PAIR_STAGE_BYTES = 2 * 128 * MM_BK;   // this CTA's halves of A and B
-constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 1;
-constexpr int PAIR_PITCH = 36;                      // floats of a row of an output slice
-constexpr int PAIR_OUT = 8 * 32 * PAIR_PITCH;       // a 32 x 32 slice per promotion warp
-constexpr size_t PAIR_SMEM = 1024 + (size_t)PAIR_STAGES * PAIR_STAGE_BYTES + sizeof(float) * PAIR_OUT +
-                             8 * PAIR_BARS + 64;
-static_assert(PAIR_SMEM <= 232448, "fits the shared memory of one CTA");
-constexpr int PAIR_GROUP = 8;   // tile rows that are walked together, column by column
+constexpr int WIDE_THREADS = 384;
+constexpr int WIDE_STAGES = 4;
+constexpr int WIDE_A_BYTES = 128 * MM_BK;
+constexpr int WIDE_STAGE_BYTES = 3 * 128 * MM_BK;
+constexpr int WIDE_BARS = 2 * WIDE_STAGES + 4 + 1;
+constexpr int WIDE_PITCH = 80;                      // bytes of a row of an output slice: 64 and a gap
+constexpr int WIDE_OUT = 8 * 32 * WIDE_PITCH;       // a slice of 32 rows per promotion warp
+constexpr size_t WIDE_SMEM = 1024 + (size_t)WIDE_STAGES * WIDE_STAGE_BYTES + WIDE_OUT +
+                             8 * WIDE_BARS + 64;
+static_assert(WIDE_SMEM <= 232448, "fits the shared memory of one CTA");
+constexpr int WIDE_GROUP = 16;   // tile rows that are walked together, column by column
 
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
-        "l"(adesc), "l"(bdesc), "r"(mm_idesc(256, 256)), "r"(accumulate));
-}
-// Tile t in groups of PAIR_GROUP tile rows, so that the tiles in flight share rows and columns
+// Tile t in groups of WIDE_GROUP tile rows, so that the tiles in flight share rows and columns
 // that the L2 holds.
-__device__ __forceinline__ void pair_tile(const MmArgs &a, int t, int &tm, int &tn) {
-    const int per = PAIR_GROUP * a.tiles_n, g = t / per, r = t - g * per;
-    const int h = min(PAIR_GROUP, a.tiles_m - g * PAIR_GROUP);
+__device__ __forceinline__ void wide_tile(const MmArgs &a, int t, int &tm, int &tn) {
+    const int per = WIDE_GROUP * a.tiles_n, g = t / per, r = t - g * per;
+    const int h = min(WIDE_GROUP, a.tiles_m - g * WIDE_GROUP);
     tn = r / h;
-    tm = g * PAIR_GROUP + (r - tn * h);
+    tm = g * WIDE_GROUP + (r - tn * h);
 }
 
 // The two scales of blocks kb .. kb + 3 (those that are there). The product is taken a group of
@@ -666,42 +673,67 @@ struct Scales4 {
     }
 };
 
+// acc += s * the 128 columns at taddr, 32 at a time, the next 32 on their way meanwhile; the
+// accumulator is released when the last have arrived.
+__device__ __forceinline__ void wide_promote(uint32_t taddr, float s, float (&acc)[128],
+                                             uint64_t *release, int lane) {
+    uint32_t r0[32], r1[32];
+    __syncwarp();
+    tc_fence_after();
+    mm_ld32(taddr, r0);
+    mm_wait_ld32(r0);
+    mm_ld32(taddr + 32, r1);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(r0[j]), s, acc[j]);
+    mm_wait_ld32(r1);
+    mm_ld32(taddr + 64, r0);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[32 + j] = fmaf(__uint_as_float(r1[j]), s, acc[32 + j]);
+    mm_wait_ld32(r0);
+    mm_ld32(taddr + 96, r1);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[64 + j] = fmaf(__uint_as_float(r0[j]), s, acc[64 + j]);
+    mm_wait_ld32(r1);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(release);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[96 + j] = fmaf(__uint_as_float(r1[j]), s, acc[96 + j]);
+}
+
 template <typename TY>
-__global__ void __launch_bounds__(PAIR_THREADS, 1)
-fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ MmArgs a) {
     extern __shared__ __align__(1024) unsigned char mm_smem[];
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
-    float *out = reinterpret_cast<float *>(stages + PAIR_STAGES * PAIR_STAGE_BYTES);
-    uint64_t *full = reinterpret_cast<uint64_t *>(out + PAIR_OUT);   // the leader's
-    uint64_t *empty = full + PAIR_STAGES;
-    uint64_t *acc_full = empty + PAIR_STAGES;   // 2
-    uint64_t *acc_empty = acc_full + 2;         // 2, the leader's
+    unsigned char *out = stages + WIDE_STAGES * WIDE_STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(out + WIDE_OUT);
+    uint64_t *empty = full + WIDE_STAGES;
+    uint64_t *acc_full = empty + WIDE_STAGES;   // 2
+    uint64_t *acc_empty = acc_full + 2;         // 2
     uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = tc::cluster_rank();
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int tiles = a.tiles_m * a.tiles_n;
 
     if (warp == 0) {
-        for (int i = lane; i < PAIR_BARS; i += 32) {
+        for (int i = lane; i < WIDE_BARS; i += 32) {
             uint64_t *b = full + i;
-            mbar_init(b, b >= acc_empty && b < mma_done ? 16u : 1u);
+            mbar_init(b, b >= acc_empty && b < mma_done ? 8u : 1u);
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
     } else if (warp == 1) {
-        tc::tmem_alloc_pair(tmem_slot, 512);
-        tc::tmem_relinquish_pair();
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive or TMA
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_next();
@@ -711,132 +743,120 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             const bool one = elect_one();
-            Ring<PAIR_STAGES> st;
+            Ring<WIDE_STAGES> st;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += npairs) {
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 int tm, tn;
-                pair_tile(a, t, tm, tn);
-                const int ya = tm * 256 + 128 * (int)rank, yb = tn * 256 + 128 * (int)rank;
+                wide_tile(a, t, tm, tn);
                 for (int kb = 0; kb < a.kb; ++kb, st.next()) {
                     ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 31);
                     if (!ok) break;
                     if (one) {
-                        unsigned char *sa = stages + st.i * PAIR_STAGE_BYTES;
-                        // the leader's barrier counts both CTAs' bytes
-                        if (rank == 0) mbar_expect_tx(&full[st.i], 2 * PAIR_STAGE_BYTES);
-                        const uint32_t fb = tc::map_to_rank(&full[st.i], 0);
-                        tc::tma_load_2d_pair(&amap, fb, sa, kb * MM_BK, ya);
-                        tc::tma_load_2d_pair(&bmap, fb, sa + 128 * MM_BK, kb * MM_BK, yb);
+                        unsigned char *sa = stages + st.i * WIDE_STAGE_BYTES;
+                        mbar_expect_tx(&full[st.i], WIDE_STAGE_BYTES);
+                        tma_load_2d(&amap, &full[st.i], sa, kb * MM_BK, tm * 128);
+                        tma_load_2d(&bmap, &full[st.i], sa + WIDE_A_BYTES, kb * MM_BK, tn * 256);
                     }
                     __syncwarp();
                 }
             }
             if (!ok) mm_drain();
         } else if (warp == 1) {
-            if (rank == 0) {
-                const bool one = elect_one();
-                Ring<PAIR_STAGES> st;
-                Ring<2> b;
-                bool ok = true;
-                for (int t = pair; t < tiles && ok; t += npairs) {
-                    for (int kb = 0; kb < a.kb; ++kb, st.next(), b.next()) {
-                        ok = mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 32) &&
-                             mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 33);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (one) {
-                            const uint32_t w = smem_u32(stages + st.i * PAIR_STAGE_BYTES);
-                            const uint64_t ad = mm_desc(w), bd = mm_desc(w + 128 * MM_BK);
+            const bool one = elect_one();
+            Ring<WIDE_STAGES> st;
+            Ring<2> b;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                for (int kb = 0; kb < a.kb; ++kb, st.next(), b.next()) {
+                    ok = mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 32) &&
+                         mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 33);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (one) {
+                        const uint32_t w = smem_u32(stages + st.i * WIDE_STAGE_BYTES);
+                        const uint64_t ad = mm_desc(w), bd = mm_desc(w + WIDE_A_BYTES);
 #pragma unroll
-                            for (int k = 0; k < MM_BK / 32; ++k)
-                                mma_e4m3_pair(tmem + (uint32_t)(b.i * 256), ad + 2 * k, bd + 2 * k, k > 0);
-                            tc::mma_commit_pair(&empty[st.i], 0x3);
-                            tc::mma_commit_pair(&acc_full[b.i], 0x3);
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < MM_BK / 32; ++k)
+                            mma_e4m3(tmem + (uint32_t)(b.i * 256), ad + 2 * k, bd + 2 * k,
+                                     mm_idesc(128, 256), k > 0);
+                        mma_commit(&acc_full[b.i]);
+                        mma_commit(&empty[st.i]);
                     }
+                    __syncwarp();
                 }
-                // all MMAs complete before the pair's TMEM is released
-                if (one) tc::mma_commit_pair(mma_done, 0x1);
-                mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
             }
+            // all MMAs complete before the TMEM is released
+            if (one) mma_commit(mma_done);
+            mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int q = warp & 3, h = (warp - 4) >> 2;
-        const uint32_t te0 = tc::map_to_rank(&acc_empty[0], 0), te1 = tc::map_to_rank(&acc_empty[1], 0);
-        float *slice = out + (warp - 4) * 32 * PAIR_PITCH;
-        Ring<2> b;
-        bool ok = true;
+        unsigned char *slice = out + (warp - 4) * 32 * WIDE_PITCH;
+        uint32_t n = 0;   // blocks so far: accumulator n & 1
+        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * h);
         const bool vec = (a.kb & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15u) == 0;
-        for (int t = pair; t < tiles; t += npairs) {
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             int tm, tn;
-            pair_tile(a, t, tm, tn);
-            const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
+            wide_tile(a, t, tm, tn);
+            const int m0 = tm * 128 + 32 * q, n0 = tn * 256 + 128 * h;
             // rows and columns behind the last take its scales: what they scale is not stored
             const float *pa = a.sA + (long long)min(m0 + lane, a.m - 1) * a.kb;
             const float *pb = a.sB + (long long)min(2 * tn + h, a.nb128 - 1) * a.kb;
             Scales4 next = {};
             next.load(pa, pb, 0, a.kb, vec);
-            float4 sc = {};
-            uint64_t acc[64];   // 128 columns of one row, in pairs
+            float acc[128];   // 128 columns of one row
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
-            for (int kb = 0; kb < a.kb; ++kb, b.next()) {
-                if ((kb & 3) == 0) {
-                    sc = next.product();
-                    next.load(pa, pb, kb + 4, a.kb, vec);
+            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+#pragma unroll 1
+            for (int kb = 0; kb < a.kb; kb += 4) {
+                const float4 sc = next.product();
+                next.load(pa, pb, kb + 4, a.kb, vec);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u > 0 && kb + u >= a.kb) break;
+                    // no way out after an abort (its later waits return at once): a branch that
+                    // leaves the loop made the compiler move the 128 sums about
+                    mm_wait(&acc_full[n & 1], (n >> 1) & 1, a.wait_limit, abort_flag, 35);
+                    wide_promote(tq + (n & 1) * 256, u == 0 ? sc.x : u == 1 ? sc.y : u == 2 ? sc.z : sc.w,
+                                 acc, &acc_empty[n & 1], lane);
+                    ++n;
                 }
-                const float s = sc.x;
-                sc.x = sc.y; sc.y = sc.z; sc.z = sc.w;
-                ok = mm_wait(&acc_full[b.i], b.phase, a.wait_limit, abort_flag, 37);
-                if (!ok) break;
-                __syncwarp();
-                tc_fence_after();
-                const uint64_t s2 = pair_of(s, s);
-                const uint32_t tt = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b.i * 256 + 128 * h);
-                uint32_t r0[32], r1[32];
-                mm_ld32(tt, r0);
-                mm_wait_ld32(r0);
-                mm_ld32(tt + 32, r1);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[j], r0[2 * j], r0[2 * j + 1], s2);
-                mm_wait_ld32(r1);
-                mm_ld32(tt + 64, r0);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[16 + j], r1[2 * j], r1[2 * j + 1], s2);
-                mm_wait_ld32(r0);
-                mm_ld32(tt + 96, r1);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[32 + j], r0[2 * j], r0[2 * j + 1], s2);
-                mm_wait_ld32(r1);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mm_arrive_remote(b.i ? te1 : te0);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[48 + j], r1[2 * j], r1[2 * j + 1], s2);
             }
-            if (!ok) break;
-            // 32 columns at a time through shared memory: rows of the slice leave as whole sectors
+            // 64 bytes of a row at a time through shared memory, so that stores cover whole sectors
+            constexpr int E = 16 / sizeof(TY), C = 4 * E;   // values of 16 and of 64 bytes
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (n0 + 32 * c >= a.n || m0 >= a.m) continue;   // the same in the whole warp
+            for (int c = 0; c < 128 / C; ++c) {
+                if (n0 + C * c >= a.n || m0 >= a.m) continue;   // the same in the whole warp
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float2 u = unpair(acc[16 * c + j]), v = unpair(acc[16 * c + j + 1]);
-                    *reinterpret_cast<float4 *>(slice + lane * PAIR_PITCH + 2 * j) =
-                        make_float4(u.x, u.y, v.x, v.y);
+                for (int j = 0; j < 4; ++j) {
+                    TY v[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] = narrow<TY>(acc[C * c + E * j + e]);
+                    *reinterpret_cast<uint4 *>(slice + lane * WIDE_PITCH + 16 * j) =
+                        *reinterpret_cast<const uint4 *>(v);
                 }
                 __syncwarp();
-                const int col = n0 + 32 * c + 4 * (lane & 7);
+                TY *y = static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0 + C * c;
+                if (a.vec16 && n0 + C * c + C <= a.n) {
+                    y += (long long)(lane >> 2) * a.ldy + E * (lane & 3);
 #pragma unroll
-                for (int r = lane >> 3; r < 32; r += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(slice + r * PAIR_PITCH + 4 * (lane & 7));
-                    if (m0 + r < a.m && col < a.n)
-                        store_y4(static_cast<TY *>(a.Y) + (long long)(m0 + r) * a.ldy + col, col, a.n,
-                                 a.vec, v);
+                    for (int r = 0; r < 32; r += 8, y += 8 * a.ldy) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(
+                            slice + (r + (lane >> 2)) * WIDE_PITCH + 16 * (lane & 3));
+                        if (m0 + r + (lane >> 2) < a.m) *reinterpret_cast<uint4 *>(y) = w;
+                    }
+                } else {   // neighbouring lanes store neighbouring columns
+                    const int col = lane % C, dr = lane / C;
+                    y += (long long)dr * a.ldy + col;
+#pragma unroll 4
+                    for (int r = 0; r < 32; r += 32 / C, y += (32 / C) * a.ldy) {
+                        const TY w = *reinterpret_cast<const TY *>(slice + (r + dr) * WIDE_PITCH +
+                                                                   sizeof(TY) * col);
+                        if (m0 + r + dr < a.m && n0 + C * c + col < a.n) *y = w;
+                    }
                 }
                 __syncwarp();
             }
@@ -844,9 +864,8 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // the peer's TMEM, barriers and shared memory outlive every access
     tc_fence_after();
-    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -895,16 +914,15 @@ inline int mm_resident(int size) {
     const int sms = device_sm_count();
     return sms >= 148 ? on148[size] : sms / size * size * 3 / 4;
 }
-// Parts of K for `tiles` tiles: the fewest blocks on the critical path, rounds of CTAs x blocks of
-// a CTA, with `extra` blocks' time for the reduction.
-inline int mm_split(long long tiles, int kb, int extra, long long &cost) {
+// Parts of K for `tiles` tiles: the least cost, rounds of CTAs x (blocks of a CTA and what a round
+// costs besides) and what adding the parts up costs; all in blocks of a CTA.
+inline int mm_split(long long tiles, int kb, int round, int add, long long &cost) {
     int best = 1;
     cost = -1;
     for (int s = 1; s <= 8 && s <= kb; ++s) {
         const int at_once = mm_resident(s) / s * s;
         if (at_once < s) continue;
-        const long long rounds = (tiles * s + at_once - 1) / at_once;
-        const long long c = rounds * ((kb + s - 1) / s + extra + (s > 1 ? extra : 0));
+        const long long c = (tiles * s + at_once - 1) / at_once * ((kb + s - 1) / s + round) + (s > 1 ? add : 0);
         if (cost < 0 || c < cost) { cost = c; best = s; }
     }
     return best;
@@ -915,16 +933,11 @@ inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb,
                      MmArgs a, cudaStream_t s) {
     using S = NarrowShape<NT>;
     a.tiles_m = ceil_div(a.m, NT);
-    // 64 rows a CTA where that leaves fewer bytes on the critical path: half the bytes a block
-    long long c128, c64;
-    const int s128 = mm_split((long long)ceil_div(a.n, 128) * a.tiles_m, a.kb, 4, c128);
-    const int s64 = mm_split((long long)ceil_div(a.n, 64) * a.tiles_m, a.kb, 6, c64);
-    const bool half = 2 * c64 < 3 * c128 && a.n > 64;
-    a.rows = half ? 64 : 128;
-    a.split = half ? s64 : s128;
-    a.tiles_n = ceil_div(a.n, a.rows);
+    a.tiles_n = ceil_div(a.n, 128);
+    long long cost;   // a block 0.24 us, a round 3 us, the sum over the cluster 0.5 us
+    a.split = mm_split((long long)a.tiles_n * a.tiles_m, a.kb, 12, 2, cost);
     CUtensorMap wmap, xmap;
-    if (!mm_map(&wmap, B, a.n, k, ldb, a.rows) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
+    if (!mm_map(&wmap, B, a.n, k, ldb, 128) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_narrow_kernel<NT, TY>;
     GPTQ_SMEM_LIMIT(kernel, S::SMEM);
     return mm_launch(kernel, (long long)a.tiles_n * a.tiles_m * a.split, a.split, NARROW_THREADS, S::SMEM,
@@ -933,11 +946,10 @@ inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb,
 
 template <typename TY>
 inline int mm_tile(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
-                   cudaStream_t s) {
+                   int split, cudaStream_t s) {
     a.tiles_m = ceil_div(a.m, 128);
     a.tiles_n = ceil_div(a.n, 128);
-    long long cost;
-    a.split = mm_split((long long)a.tiles_m * a.tiles_n, a.kb, 4, cost);
+    a.split = split;
     CUtensorMap amap, bmap;
     if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_tile_kernel<TY>;
@@ -947,30 +959,38 @@ inline int mm_tile(const void *A, long long lda, const void *B, long long ldb, l
 }
 
 template <typename TY>
-inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
+inline int mm_wide(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
                    cudaStream_t s) {
-    a.tiles_m = ceil_div(a.m, 256);
+    a.tiles_m = ceil_div(a.m, 128);
     a.tiles_n = ceil_div(a.n, 256);
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
     if (tiles > 0x7fffffffLL - 1024) return GPTQ_ERR_ARG;
     a.split = 1;
     CUtensorMap amap, bmap;
-    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
-    auto kernel = fp8_mm_pair_kernel<TY>;
-    GPTQ_SMEM_LIMIT(kernel, PAIR_SMEM);
-    const long long pairs = std::min<long long>(tiles, device_sm_count() / 2);
-    return mm_launch(kernel, 2 * pairs, 2, PAIR_THREADS, PAIR_SMEM, amap, bmap, a, s);
+    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 256)) return GPTQ_ERR_CUDA;
+    auto kernel = fp8_mm_wide_kernel<TY>;
+    GPTQ_SMEM_LIMIT(kernel, WIDE_SMEM);
+    const long long ctas = std::min<long long>(tiles, device_sm_count());
+    return mm_launch(kernel, ctas, 1, WIDE_THREADS, WIDE_SMEM, amap, bmap, a, s);
 }
 
 template <typename TY>
 inline int mm_type(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
                    cudaStream_t s) {
+    // up to 32 rows the narrow kernel: 1 x 2048 x 6144 5.9 us, 32 rows 7.7 us (tile kernel 10.2 us);
+    // at 64 rows of 6144 x 2048 the tile kernel is ahead, 9.0 us to 11.4 us
     if (a.m <= 16) return mm_narrow<16, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 32) return mm_narrow<32, TY>(A, lda, B, ldb, k, a, s);
-    if (a.m <= 64) return mm_narrow<64, TY>(A, lda, B, ldb, k, a, s);
-    const long long pair_tiles = (long long)ceil_div(a.m, 256) * ceil_div(a.n, 256);
-    if (pair_tiles >= device_sm_count() / 2) return mm_pair<TY>(A, lda, B, ldb, k, a, s);
-    return mm_tile<TY>(A, lda, B, ldb, k, a, s);
+    // The tile kernel takes 0.22 us a block, 4.5 us a round of CTAs, 2.5 us for the sum over a
+    // cluster; the wide kernel (twice the columns) 0.44 us a block, 2.7 us a tile and 3.5 us once.
+    // Where rounds are even the larger tile wins: 2048 x 2048 x 6144 27 us to 38 us, 777 x 1500 x 2900
+    // 16 us to 13 us.
+    long long tile;
+    const int split = mm_split((long long)ceil_div(a.m, 128) * ceil_div(a.n, 128), a.kb, 20, 11, tile);
+    const long long tiles = (long long)ceil_div(a.m, 128) * ceil_div(a.n, 256), sms = device_sm_count();
+    const long long wide = (tiles + sms - 1) / sms * (2 * a.kb + 12) + 16;
+    if (wide < tile) return mm_wide<TY>(A, lda, B, ldb, k, a, s);
+    return mm_tile<TY>(A, lda, B, ldb, k, a, split, s);
 }
 
 inline int fp8_matmul(const void *A, long long lda, const float *sA, const void *B, long long ldb,
@@ -990,6 +1010,7 @@ inline int fp8_matmul(const void *A, long long lda, const float *sA, const void 
     a.kb = (int)((k + MM_BK - 1) / MM_BK);
     a.nb128 = ceil_div(n, 128);
     a.vec = ldy % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % (4 * size) == 0;
+    a.vec16 = ldy * size % 16 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
     // a wait longer than ~2 s at the 1.9 GHz clock means a lost signal, not a slow kernel
     a.wait_limit = tc::env_ll("GPTQ_WAIT_LIMIT_CYCLES", 4000000000LL);
     switch (y_dtype) {
