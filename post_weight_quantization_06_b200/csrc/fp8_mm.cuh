@@ -8,6 +8,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "hessian_tc.cuh"
 #include "serve_common.cuh"
@@ -191,6 +192,41 @@ __device__ __forceinline__ void store_y4(TY *y, int col, int n, float4 v) {
             if (col + i < n) y[i] = t[i];
     }
 }
+// 32 rows x 128 bytes of shared memory in the 128-byte swizzle to Y at (x, y); one bulk group.
+__device__ __forceinline__ void mm_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(smem_u32(src)), "r"(x), "r"(y)
+        : "memory");
+}
+// The same slice by ordinary stores, for rows of Y that TMA does not take (a pitch that is no
+// multiple of 16 bytes): `rows` rows, `cols` columns from y on, one value a lane. (32-bit words,
+// with the single 16-bit values that rows starting between two words need at their ends, took twice
+// as long: 5000 x 3001 x 777 58 us to 32 us.)
+template <typename TY>
+__device__ __forceinline__ void store_slice(TY *y, long long ldy, const unsigned char *slice, int rows,
+                                            int cols, int lane) {
+    constexpr int AT_ONCE = 8;   // rows whose values are on their way from shared memory together
+    constexpr int S = 4 / sizeof(TY);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += AT_ONCE) {
+        TY w[AT_ONCE][S];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)   // r0 is a multiple of 8: row r0 + i has swizzle i
+#pragma unroll
+            for (int h = 0; h < S; ++h) {
+                const int at = (lane + 32 * h) * (int)sizeof(TY);
+                w[i][h] = *reinterpret_cast<const TY *>(slice + (r0 + i) * 128 + (at ^ (i << 4)));
+            }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i, y += ldy)
+#pragma unroll
+            for (int h = 0; h < S; ++h)
+                if (r0 + i < rows && lane + 32 * h < cols) y[lane + 32 * h] = w[i][h];
+    }
+}
+
 struct MmArgs {
     const float *sA, *sB;
     void *Y;
@@ -199,7 +235,7 @@ struct MmArgs {
     int nb128;               // blocks of 128 columns of Y
     int tiles_m, tiles_n;
     int split;               // CTAs of a cluster, each with a part of the K blocks
-    int vec, vec16;          // four values, or 16 bytes, of Y can be stored at once
+    int vec, vec16;          // four values can be stored at once; TMA takes the rows of Y
     long long wait_limit;
 };
 
@@ -619,36 +655,42 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 }
 
 // ---------------------------------------------------------------------------------------
-// Many rows: 128 x 256 tiles of Y, persistent, one CTA per SM. A block of K takes the tensor cores
-// 512 cycles (four 128 x 256 x 32 MMAs into one of two accumulators); in that time a promotion
-// thread reads the 128 columns of its row from the other one and adds them to 128 sums in
-// registers (setmaxnreg: 232 for the promotion warps, 40 for the others, together the 168 x 384
-// of the launch). Its row's scales come straight from memory, four blocks at a time and a group
-// ahead. With two accumulators what counts is the way from a block's last MMA to the release of
-// its accumulator: a CTA pair (cta_group::2), which moves two thirds of the bytes, takes 930 cycles
-// a block, since commits and arrivals cross to the other SM; this one takes 820.
+// Many rows: 256 x 256 tiles of Y by a CTA pair (tcgen05 cta_group::2), persistent. CTA r holds
+// rows 128 r .. of the pair's A and B; the leader's 256 x 256 x 32 MMAs read both CTAs' shared
+// memory and leave rows 128 r .. of the tile in CTA r's TMEM. A block of K takes the tensor cores
+// 512 cycles; in that time a promotion thread reads 128 columns of its row from one of two
+// accumulators and adds them to 128 sums in registers (setmaxnreg: 232 for the promotion warps,
+// 40 for the others, together the 168 x 384 of the launch). Its row's scales come straight from
+// memory, four blocks at a time and a group ahead.
 //
-// Warps: 0 TMA, 1 TMEM and MMA, 4-11 promotion (32 rows x 128 columns each).
+// With two accumulators (all of TMEM) what bounds a block is the way from its last MMA to the
+// release of its accumulator, about PAIR_CYCLES cycles, then the 1000 W power limit. One CTA per
+// 128 x 256 tile has the shorter way (its commits and arrivals stay on the SM) but moves half as
+// much again; on random data it was 6 % slower. Accumulators of 128 columns, four of them, were
+// slower still: every wait and arrival doubles.
+//
+// Warps: 0 TMA, 1 TMEM and (leader) MMA, 4-11 promotion (32 rows x 128 columns each). A tile's sums
+// are rounded into shared memory and leave by TMA while the next tile runs.
 // ---------------------------------------------------------------------------------------
-constexpr int WIDE_THREADS = 384;
-constexpr int WIDE_STAGES = 4;
-constexpr int WIDE_A_BYTES = 128 * MM_BK;
-constexpr int WIDE_STAGE_BYTES = 3 * 128 * MM_BK;
-constexpr int WIDE_BARS = 2 * WIDE_STAGES + 4 + 1;
-constexpr int WIDE_PITCH = 80;                      // bytes of a row of an output slice: 64 and a gap
-constexpr int WIDE_OUT = 8 * 32 * WIDE_PITCH;       // a slice of 32 rows per promotion warp
-constexpr size_t WIDE_SMEM = 1024 + (size_t)WIDE_STAGES * WIDE_STAGE_BYTES + WIDE_OUT +
-                             8 * WIDE_BARS + 64;
-static_assert(WIDE_SMEM <= 232448, "fits the shared memory of one CTA");
-constexpr int WIDE_GROUP = 16;   // tile rows that are walked together, column by column
+constexpr int PAIR_THREADS = 384;
+constexpr int PAIR_STAGES = 5;
+constexpr int PAIR_A_BYTES = 128 * MM_BK;
+constexpr int PAIR_STAGE_BYTES = 2 * 128 * MM_BK;   // this CTA's halves of A and B
+constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 1;
+constexpr int PAIR_SLICE = 32 * 128;                // 128 bytes of 32 rows, 128-byte swizzle
+constexpr int PAIR_OUT = 8 * 2 * PAIR_SLICE;        // two slices per promotion warp
+constexpr size_t PAIR_SMEM = 1024 + (size_t)PAIR_STAGES * PAIR_STAGE_BYTES + PAIR_OUT +
+                             8 * PAIR_BARS + 64;
+static_assert(PAIR_SMEM <= 232448, "fits the shared memory of one CTA");
+constexpr int PAIR_GROUP = 8;   // tile rows that are walked together, column by column
 
-// Tile t in groups of WIDE_GROUP tile rows, so that the tiles in flight share rows and columns
+// Tile t in groups of PAIR_GROUP tile rows, so that the tiles in flight share rows and columns
 // that the L2 holds.
-__device__ __forceinline__ void wide_tile(const MmArgs &a, int t, int &tm, int &tn) {
-    const int per = WIDE_GROUP * a.tiles_n, g = t / per, r = t - g * per;
-    const int h = min(WIDE_GROUP, a.tiles_m - g * WIDE_GROUP);
+__device__ __forceinline__ void pair_tile(const MmArgs &a, int t, int &tm, int &tn) {
+    const int per = PAIR_GROUP * a.tiles_n, g = t / per, r = t - g * per;
+    const int h = min(PAIR_GROUP, a.tiles_m - g * PAIR_GROUP);
     tn = r / h;
-    tm = g * WIDE_GROUP + (r - tn * h);
+    tm = g * PAIR_GROUP + (r - tn * h);
 }
 
 // The two scales of blocks kb .. kb + 3 (those that are there). The product is taken a group of
@@ -673,10 +715,24 @@ struct Scales4 {
     }
 };
 
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
+        "l"(adesc), "l"(bdesc), "r"(mm_idesc(256, 256)), "r"(accumulate));
+}
+// Arrival on a barrier of the pair's leader. What it orders are TMEM loads that have completed
+// (tcgen05.wait::ld), so the default scope will do: a release at cluster scope fences the thread's
+// memory first and cost the promotion a thousand cycles a block.
+__device__ __forceinline__ void mm_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // acc += s * the 128 columns at taddr, 32 at a time, the next 32 on their way meanwhile; the
 // accumulator is released when the last have arrived.
-__device__ __forceinline__ void wide_promote(uint32_t taddr, float s, float (&acc)[128],
-                                             uint64_t *release, int lane) {
+__device__ __forceinline__ void pair_promote(uint32_t taddr, float s, float (&acc)[128],
+                                             uint32_t release, int lane) {
     uint32_t r0[32], r1[32];
     __syncwarp();
     tc_fence_after();
@@ -696,22 +752,22 @@ __device__ __forceinline__ void wide_promote(uint32_t taddr, float s, float (&ac
     mm_wait_ld32(r1);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(release);
+    if (lane == 0) mm_arrive_remote(release);
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[96 + j] = fmaf(__uint_as_float(r1[j]), s, acc[96 + j]);
 }
 
 template <typename TY>
-__global__ void __launch_bounds__(WIDE_THREADS, 1)
-fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                   const __grid_constant__ MmArgs a) {
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ CUtensorMap ymap, const __grid_constant__ MmArgs a) {
     extern __shared__ __align__(1024) unsigned char mm_smem[];
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
-    unsigned char *out = stages + WIDE_STAGES * WIDE_STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(out + WIDE_OUT);
-    uint64_t *empty = full + WIDE_STAGES;
-    uint64_t *acc_full = empty + WIDE_STAGES;   // 2
+    unsigned char *out = stages + PAIR_STAGES * PAIR_STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(out + PAIR_OUT);
+    uint64_t *empty = full + PAIR_STAGES;
+    uint64_t *acc_full = empty + PAIR_STAGES;   // 2
     uint64_t *acc_empty = acc_full + 2;         // 2
     uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
@@ -719,21 +775,24 @@ fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = a.tiles_m * a.tiles_n;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0) {
-        for (int i = lane; i < WIDE_BARS; i += 32) {
+        for (int i = lane; i < PAIR_BARS; i += 32) {
             uint64_t *b = full + i;
-            mbar_init(b, b >= acc_empty && b < mma_done ? 8u : 1u);
+            mbar_init(b, b >= acc_empty && b < mma_done ? 16u : 1u);
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
     } else if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
+        tc::tmem_alloc_pair(tmem_slot, 512);
+        tc::tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive or TMA
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_next();
@@ -743,65 +802,69 @@ fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             const bool one = elect_one();
-            Ring<WIDE_STAGES> st;
+            Ring<PAIR_STAGES> st;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 int tm, tn;
-                wide_tile(a, t, tm, tn);
+                pair_tile(a, t, tm, tn);
                 for (int kb = 0; kb < a.kb; ++kb, st.next()) {
                     ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 31);
                     if (!ok) break;
                     if (one) {
-                        unsigned char *sa = stages + st.i * WIDE_STAGE_BYTES;
-                        mbar_expect_tx(&full[st.i], WIDE_STAGE_BYTES);
-                        tma_load_2d(&amap, &full[st.i], sa, kb * MM_BK, tm * 128);
-                        tma_load_2d(&bmap, &full[st.i], sa + WIDE_A_BYTES, kb * MM_BK, tn * 256);
+                        unsigned char *sa = stages + st.i * PAIR_STAGE_BYTES;
+                        // the leader's barrier counts both CTAs' bytes
+                        if (rank == 0) mbar_expect_tx(&full[st.i], 2 * PAIR_STAGE_BYTES);
+                        const uint32_t fb = tc::map_to_rank(&full[st.i], 0);
+                        const int r0 = 128 * (int)rank;
+                        tc::tma_load_2d_pair(&amap, fb, sa, kb * MM_BK, tm * 256 + r0);
+                        tc::tma_load_2d_pair(&bmap, fb, sa + PAIR_A_BYTES, kb * MM_BK, tn * 256 + r0);
                     }
                     __syncwarp();
                 }
             }
             if (!ok) mm_drain();
-        } else if (warp == 1) {
+        } else if (warp == 1 && rank == 0) {
             const bool one = elect_one();
-            Ring<WIDE_STAGES> st;
+            Ring<PAIR_STAGES> st;
             Ring<2> b;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int kb = 0; kb < a.kb; ++kb, st.next(), b.next()) {
                     ok = mm_wait(&full[st.i], st.phase, a.wait_limit, abort_flag, 32) &&
                          mm_wait(&acc_empty[b.i], b.phase ^ 1u, a.wait_limit, abort_flag, 33);
                     if (!ok) break;
                     tc_fence_after();
                     if (one) {
-                        const uint32_t w = smem_u32(stages + st.i * WIDE_STAGE_BYTES);
-                        const uint64_t ad = mm_desc(w), bd = mm_desc(w + WIDE_A_BYTES);
+                        const uint32_t w = smem_u32(stages + st.i * PAIR_STAGE_BYTES);
+                        const uint64_t ad = mm_desc(w), bd = mm_desc(w + PAIR_A_BYTES);
 #pragma unroll
                         for (int k = 0; k < MM_BK / 32; ++k)
-                            mma_e4m3(tmem + (uint32_t)(b.i * 256), ad + 2 * k, bd + 2 * k,
-                                     mm_idesc(128, 256), k > 0);
-                        mma_commit(&acc_full[b.i]);
-                        mma_commit(&empty[st.i]);
+                            mma_e4m3_pair(tmem + (uint32_t)(b.i * 256), ad + 2 * k, bd + 2 * k, k > 0);
+                        tc::mma_commit_pair(&acc_full[b.i], 0x3);
+                        tc::mma_commit_pair(&empty[st.i], 0x3);
                     }
                     __syncwarp();
                 }
             }
             // all MMAs complete before the TMEM is released
-            if (one) mma_commit(mma_done);
+            if (one) tc::mma_commit_pair(mma_done, 0x1);
             mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int q = warp & 3, h = (warp - 4) >> 2;
-        unsigned char *slice = out + (warp - 4) * 32 * WIDE_PITCH;
+        unsigned char *slices = out + (warp - 4) * 2 * PAIR_SLICE;
+        int turn = 0;
+        const uint32_t release = tc::map_to_rank(acc_empty, 0);
         uint32_t n = 0;   // blocks so far: accumulator n & 1
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * h);
         const bool vec = (a.kb & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15u) == 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        for (int t = pair; t < tiles; t += pairs) {
             int tm, tn;
-            wide_tile(a, t, tm, tn);
-            const int m0 = tm * 128 + 32 * q, n0 = tn * 256 + 128 * h;
+            pair_tile(a, t, tm, tn);
+            const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
             // rows and columns behind the last take its scales: what they scale is not stored
             const float *pa = a.sA + (long long)min(m0 + lane, a.m - 1) * a.kb;
             const float *pb = a.sB + (long long)min(2 * tn + h, a.nb128 - 1) * a.kb;
@@ -820,52 +883,49 @@ fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                     // no way out after an abort (its later waits return at once): a branch that
                     // leaves the loop made the compiler move the 128 sums about
                     mm_wait(&acc_full[n & 1], (n >> 1) & 1, a.wait_limit, abort_flag, 35);
-                    wide_promote(tq + (n & 1) * 256, u == 0 ? sc.x : u == 1 ? sc.y : u == 2 ? sc.z : sc.w,
-                                 acc, &acc_empty[n & 1], lane);
+                    pair_promote(tq + (n & 1) * 256, u == 0 ? sc.x : u == 1 ? sc.y : u == 2 ? sc.z : sc.w,
+                                 acc, release + 8 * (n & 1), lane);
                     ++n;
                 }
             }
-            // 64 bytes of a row at a time through shared memory, so that stores cover whole sectors
-            constexpr int E = 16 / sizeof(TY), C = 4 * E;   // values of 16 and of 64 bytes
+            // 128 bytes of a row at a time: rounded, written to a slice, and on their way
+            constexpr int E = 16 / sizeof(TY), C = 8 * E;   // values of 16 and of 128 bytes
 #pragma unroll
             for (int c = 0; c < 128 / C; ++c) {
                 if (n0 + C * c >= a.n || m0 >= a.m) continue;   // the same in the whole warp
+                // the slices take turns: the last store but one, from this one, has read it
+                unsigned char *slice = slices + (turn & 1) * PAIR_SLICE;
+                ++turn;
+                if (a.vec16 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     TY v[E];
 #pragma unroll
                     for (int e = 0; e < E; ++e) v[e] = narrow<TY>(acc[C * c + E * j + e]);
-                    *reinterpret_cast<uint4 *>(slice + lane * WIDE_PITCH + 16 * j) =
+                    *reinterpret_cast<uint4 *>(slice + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                         *reinterpret_cast<const uint4 *>(v);
                 }
-                __syncwarp();
-                TY *y = static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0 + C * c;
-                if (a.vec16 && n0 + C * c + C <= a.n) {
-                    y += (long long)(lane >> 2) * a.ldy + E * (lane & 3);
-#pragma unroll
-                    for (int r = 0; r < 32; r += 8, y += 8 * a.ldy) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(
-                            slice + (r + (lane >> 2)) * WIDE_PITCH + 16 * (lane & 3));
-                        if (m0 + r + (lane >> 2) < a.m) *reinterpret_cast<uint4 *>(y) = w;
-                    }
-                } else {   // neighbouring lanes store neighbouring columns
-                    const int col = lane % C, dr = lane / C;
-                    y += (long long)dr * a.ldy + col;
-#pragma unroll 4
-                    for (int r = 0; r < 32; r += 32 / C, y += (32 / C) * a.ldy) {
-                        const TY w = *reinterpret_cast<const TY *>(slice + (r + dr) * WIDE_PITCH +
-                                                                   sizeof(TY) * col);
-                        if (m0 + r + dr < a.m && n0 + C * c + col < a.n) *y = w;
-                    }
+                if (a.vec16) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mm_store_2d(&ymap, slice, n0 + C * c, m0);
+                } else {
+                    __syncwarp();
+                    store_slice(static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0 + C * c, a.ldy, slice,
+                                min(32, a.m - m0), a.n - n0 - C * c, lane);
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
+        if (a.vec16 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // the peer's TMEM, barriers and shared memory outlive every access
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -884,9 +944,26 @@ inline bool mm_map(CUtensorMap *map, const void *p, long long rows, long long k,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K>
-inline int mm_launch(K kernel, long long ctas, int cluster, int threads, size_t smem,
-                     const CUtensorMap &x, const CUtensorMap &y, const MmArgs &a, cudaStream_t s) {
+// Y in boxes of 32 rows x 128 bytes.
+template <typename TY>
+inline bool mm_out_map(CUtensorMap *map, const MmArgs &a) {
+    tc::EncodeTiledFn enc = tc::encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.m};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.ldy * sizeof(TY)};
+    const cuuint32_t box[2] = {128 / sizeof(TY), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapDataType t = std::is_same<TY, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : std::is_same<TY, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return enc(map, t, 2, a.Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... P, typename... V>
+inline int mm_launch(void (*kernel)(P...), long long ctas, int cluster, int threads, size_t smem,
+                     cudaStream_t s, const V &...args) {
     if (ctas > 0x7fffffffLL) return GPTQ_ERR_ARG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -901,7 +978,7 @@ inline int mm_launch(K kernel, long long ctas, int cluster, int threads, size_t 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, x, y, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     const int st = launch_status();
     return e == cudaSuccess ? st : GPTQ_ERR_CUDA;
 }
@@ -940,8 +1017,8 @@ inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb,
     if (!mm_map(&wmap, B, a.n, k, ldb, 128) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_narrow_kernel<NT, TY>;
     GPTQ_SMEM_LIMIT(kernel, S::SMEM);
-    return mm_launch(kernel, (long long)a.tiles_n * a.tiles_m * a.split, a.split, NARROW_THREADS, S::SMEM,
-                     wmap, xmap, a, s);
+    return mm_launch(kernel, (long long)a.tiles_n * a.tiles_m * a.split, a.split, NARROW_THREADS, S::SMEM, s,
+                     wmap, xmap, a);
 }
 
 template <typename TY>
@@ -954,24 +1031,25 @@ inline int mm_tile(const void *A, long long lda, const void *B, long long ldb, l
     if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_tile_kernel<TY>;
     GPTQ_SMEM_LIMIT(kernel, TILE_SMEM);
-    return mm_launch(kernel, (long long)a.tiles_m * a.tiles_n * a.split, a.split, TILE_THREADS, TILE_SMEM,
-                     amap, bmap, a, s);
+    return mm_launch(kernel, (long long)a.tiles_m * a.tiles_n * a.split, a.split, TILE_THREADS, TILE_SMEM, s,
+                     amap, bmap, a);
 }
 
 template <typename TY>
-inline int mm_wide(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
+inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
                    cudaStream_t s) {
-    a.tiles_m = ceil_div(a.m, 128);
+    a.tiles_m = ceil_div(a.m, 256);
     a.tiles_n = ceil_div(a.n, 256);
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
     if (tiles > 0x7fffffffLL - 1024) return GPTQ_ERR_ARG;
     a.split = 1;
-    CUtensorMap amap, bmap;
-    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 256)) return GPTQ_ERR_CUDA;
-    auto kernel = fp8_mm_wide_kernel<TY>;
-    GPTQ_SMEM_LIMIT(kernel, WIDE_SMEM);
-    const long long ctas = std::min<long long>(tiles, device_sm_count());
-    return mm_launch(kernel, ctas, 1, WIDE_THREADS, WIDE_SMEM, amap, bmap, a, s);
+    CUtensorMap amap, bmap, ymap = {};
+    if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
+    if (a.vec16 && !mm_out_map<TY>(&ymap, a)) return GPTQ_ERR_CUDA;
+    auto kernel = fp8_mm_pair_kernel<TY>;
+    GPTQ_SMEM_LIMIT(kernel, PAIR_SMEM);
+    const long long pairs = std::min<long long>(tiles, device_sm_count() / 2);
+    return mm_launch(kernel, 2 * pairs, 2, PAIR_THREADS, PAIR_SMEM, s, amap, bmap, ymap, a);
 }
 
 template <typename TY>
@@ -982,14 +1060,14 @@ inline int mm_type(const void *A, long long lda, const void *B, long long ldb, l
     if (a.m <= 16) return mm_narrow<16, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 32) return mm_narrow<32, TY>(A, lda, B, ldb, k, a, s);
     // The tile kernel takes 0.22 us a block, 4.5 us a round of CTAs, 2.5 us for the sum over a
-    // cluster; the wide kernel (twice the columns) 0.44 us a block, 2.7 us a tile and 3.5 us once.
+    // cluster; the pair kernel 0.44 us a block, 1 us a tile and 5 us once.
     // Where rounds are even the larger tile wins: 2048 x 2048 x 6144 27 us to 38 us, 777 x 1500 x 2900
     // 16 us to 13 us.
     long long tile;
     const int split = mm_split((long long)ceil_div(a.m, 128) * ceil_div(a.n, 128), a.kb, 20, 11, tile);
-    const long long tiles = (long long)ceil_div(a.m, 128) * ceil_div(a.n, 256), sms = device_sm_count();
-    const long long wide = (tiles + sms - 1) / sms * (2 * a.kb + 12) + 16;
-    if (wide < tile) return mm_wide<TY>(A, lda, B, ldb, k, a, s);
+    const long long tiles = (long long)ceil_div(a.m, 256) * ceil_div(a.n, 256), pairs = device_sm_count() / 2;
+    const long long pair = (tiles + pairs - 1) / pairs * (2 * a.kb + 5) + 22;
+    if (pair < tile) return mm_pair<TY>(A, lda, B, ldb, k, a, s);
     return mm_tile<TY>(A, lda, B, ldb, k, a, split, s);
 }
 
@@ -1012,7 +1090,8 @@ inline int fp8_matmul(const void *A, long long lda, const float *sA, const void 
     a.vec = ldy % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % (4 * size) == 0;
     a.vec16 = ldy * size % 16 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
     // a wait longer than ~2 s at the 1.9 GHz clock means a lost signal, not a slow kernel
-    a.wait_limit = tc::env_ll("GPTQ_WAIT_LIMIT_CYCLES", 4000000000LL);
+    static const long long wait_limit = tc::env_ll("GPTQ_WAIT_LIMIT_CYCLES", 4000000000LL);
+    a.wait_limit = wait_limit;
     switch (y_dtype) {
         case GPTQ_BF16: return mm_type<__nv_bfloat16>(A, lda, B, ldb, k, a, s);
         case GPTQ_F16: return mm_type<__half>(A, lda, B, ldb, k, a, s);

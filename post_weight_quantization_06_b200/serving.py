@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import GPTQ_BF16, GPTQ_F32, GPTQ_OK, GptqError, _lib
+from . import GPTQ_BF16, GPTQ_F32, GptqError, _lib
 
 GPTQ_F16 = 2
 GPTQ_FP8_BLOCK = 128
@@ -45,13 +45,23 @@ def _bind():
 _fp8_quantize, _fp8_matmul, _cache_write, _cache_read = _bind()
 
 
-def _stream_of(stream, tensors) -> int:
-    """The stream's handle; every tensor has to be on the current device."""
-    dev = torch.cuda.current_device()
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(stream, dev: int) -> int:
+    """The handle of the stream to run on, for tensors of device ``dev`` (which the library takes to
+    be the current one)."""
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"the tensors must be on the current device (a CUDA one), not on device {dev}")
+    return _current_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _same_device(dev: int, *tensors):
     for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}: the current device is cuda:{dev}")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"one of the tensors is on {t.device}: all must be on the "
+                             "current device")
 
 
 def _want(ok: bool, what: str):
@@ -60,7 +70,7 @@ def _want(ok: bool, what: str):
 
 
 def _typed(t: torch.Tensor, dtype, name: str):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
@@ -71,20 +81,17 @@ def _code(t: torch.Tensor) -> int:
     return c
 
 
-def _check(st: int, where: str):
-    if st != GPTQ_OK:
-        raise GptqError(st, where)
-
-
-def _rows(t: torch.Tensor, name: str) -> int:
+def _pitch(t: torch.Tensor, name: str) -> int:
     """Distance of the rows of a matrix whose columns are contiguous, in elements."""
     r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    s, one = t.stride()
+    if one != 1 and c > 1:
         raise ValueError(f"{name}: the columns must be contiguous")
-    s = t.stride(0)
-    if r > 1 and s < c:
-        raise ValueError(f"{name}: the rows must not overlap")
-    return s if s > c else c
+    if s < c:
+        if r > 1:
+            raise ValueError(f"{name}: the rows must not overlap")
+        return c
+    return s
 
 
 def gptq_fp8_quantize(X: torch.Tensor, block_rows: int, codes: torch.Tensor, scales: torch.Tensor,
@@ -94,27 +101,32 @@ def gptq_fp8_quantize(X: torch.Tensor, block_rows: int, codes: torch.Tensor, sca
     rows, cols = X.shape
     _typed(codes, _E4M3, "codes")
     _typed(scales, torch.float32, "scales")
-    _want(codes.shape == X.shape, "codes must have the shape of X")
-    _want(block_rows in (1, 128), "block_rows must be 1 or 128")
-    _want(scales.shape == (-(-rows // block_rows), -(-cols // 128)) and scales.is_contiguous(),
-          "scales must be contiguous, ceil(rows / block_rows) x ceil(cols / 128)")
-    st = _stream_of(stream, (X, codes, scales))
-    _check(_fp8_quantize(X.data_ptr(), _code(X), rows, cols, _rows(X, "X"), block_rows,
-                         codes.data_ptr(), _rows(codes, "codes"), scales.data_ptr(), st),
-           "gptq_fp8_quantize")
+    if codes.shape != X.shape:
+        raise ValueError("codes must have the shape of X")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    if scales.shape != (-(-rows // block_rows), (cols + 127) >> 7) or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous, ceil(rows / block_rows) x ceil(cols / 128)")
+    dev = X.get_device()
+    _same_device(dev, codes, scales)
+    st = _fp8_quantize(X.data_ptr(), _code(X), rows, cols, _pitch(X, "X"), block_rows,
+                       codes.data_ptr(), _pitch(codes, "codes"), scales.data_ptr(),
+                       _stream_of(stream, dev))
+    if st:
+        raise GptqError(st, "gptq_fp8_quantize")
 
 
 def fp8_quantize(X: torch.Tensor, *, block_rows: int = 1):
     """``gptq_fp8_quantize`` with fresh outputs: (codes, scales). The rows of the codes start on
     16-byte boundaries, as ``gptq_fp8_matmul`` wants them."""
     rows, cols = X.shape
-    _want(block_rows in (1, 128), "block_rows must be 1 or 128")
-    pitch = -(-cols // 16) * 16
-    codes = torch.empty((rows, pitch), dtype=_E4M3, device=X.device)
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    pitch = (cols + 15) & -16
+    codes = X.new_empty((rows, pitch), dtype=_E4M3)
     if pitch != cols:
         codes = codes[:, :cols]
-    scales = torch.empty((-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32,
-                         device=X.device)
+    scales = X.new_empty((-(-rows // block_rows), (cols + 127) >> 7), dtype=torch.float32)
     gptq_fp8_quantize(X, block_rows, codes, scales)
     return codes, scales
 
@@ -124,27 +136,33 @@ def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torc
     """Y (m x n, bf16 / fp16 / fp32) = A B^T for e4m3 codes A (m x k, scales m x ceil(k / 128))
     and B (n x k, scales ceil(n / 128) x ceil(k / 128))."""
     m, k = A.shape
-    n = B.shape[0]
-    kb = -(-k // 128)
+    n, kn = B.shape
+    kb = (k + 127) >> 7
     _typed(A, _E4M3, "A")
     _typed(B, _E4M3, "B")
     _typed(sA, torch.float32, "sA")
     _typed(sB, torch.float32, "sB")
-    _want(B.shape[1] == k, "A and B must have the same number of columns")
-    _want(sA.shape == (m, kb) and sA.is_contiguous(), "sA must be contiguous, m x ceil(k / 128)")
-    _want(sB.shape == (-(-n // 128), kb) and sB.is_contiguous(),
-          "sB must be contiguous, ceil(n / 128) x ceil(k / 128)")
-    _want(Y.shape == (m, n), "Y must be m x n")
-    st = _stream_of(stream, (A, sA, B, sB, Y))
-    _check(_fp8_matmul(A.data_ptr(), _rows(A, "A"), sA.data_ptr(), B.data_ptr(), _rows(B, "B"),
-                       sB.data_ptr(), m, n, k, Y.data_ptr(), _code(Y), _rows(Y, "Y"), st),
-           "gptq_fp8_matmul")
+    if kn != k:
+        raise ValueError("A and B must have the same number of columns")
+    if sA.shape != (m, kb) or not sA.is_contiguous():
+        raise ValueError("sA must be contiguous, m x ceil(k / 128)")
+    if sB.shape != ((n + 127) >> 7, kb) or not sB.is_contiguous():
+        raise ValueError("sB must be contiguous, ceil(n / 128) x ceil(k / 128)")
+    if Y.shape != (m, n):
+        raise ValueError("Y must be m x n")
+    dev = A.get_device()
+    _same_device(dev, sA, B, sB, Y)
+    st = _fp8_matmul(A.data_ptr(), _pitch(A, "A"), sA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
+                     sB.data_ptr(), m, n, k, Y.data_ptr(), _code(Y), _pitch(Y, "Y"),
+                     _stream_of(stream, dev))
+    if st:
+        raise GptqError(st, "gptq_fp8_matmul")
 
 
 def fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, *,
                out_dtype=torch.bfloat16) -> torch.Tensor:
     """``gptq_fp8_matmul`` into a fresh m x n tensor of ``out_dtype``."""
-    Y = torch.empty((A.shape[0], B.shape[0]), dtype=out_dtype, device=A.device)
+    Y = sA.new_empty((A.shape[0], B.shape[0]), dtype=out_dtype)
     gptq_fp8_matmul(A, sA, B, sB, Y)
     return Y
 
@@ -153,44 +171,56 @@ def _row_bytes(fmt: int, head_dim: int) -> int:
     return head_dim // 2 if fmt == GPTQ_CACHE_INT4 else head_dim
 
 
-def _cache_arrays(n_slots, heads, head_dim, fmt, group_size, arrays, two):
-    """Addresses of (codes, scales, zeros) of K and V, checked against the cache's shape."""
-    _want(group_size >= 0 and head_dim % (group_size or 1) == 0, "group_size must divide head_dim")
-    groups = head_dim // group_size if group_size else 1
-    ptrs = []
-    for i, (codes, scales, zeros) in enumerate((arrays[:3], arrays[3:])):
-        if i == 1 and not two:
-            ptrs += [None, None, None]
-            continue
-        _typed(codes, torch.uint8, "codes")
-        _typed(scales, torch.float32, "scales")
-        _want(codes.shape == (n_slots, heads, _row_bytes(fmt, head_dim)) and codes.is_contiguous(),
-              "codes must be contiguous, n_slots x heads x bytes of a head")
-        _want(scales.shape == (n_slots, heads, groups) and scales.is_contiguous(),
-              "scales must be contiguous, n_slots x heads x groups")
-        if fmt != GPTQ_CACHE_E4M3:
-            _typed(zeros, torch.uint8, "zeros")
-            _want(zeros.shape == scales.shape and zeros.is_contiguous(),
-                  "zeros must be contiguous and have the shape of scales")
-            ptrs += [codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()]
-        else:
-            ptrs += [codes.data_ptr(), scales.data_ptr(), None]
-    return ptrs
+def _cache_plane(shape, fmt, groups, codes, scales, zeros):
+    """Addresses of the codes, scales and zero-points of K or V, checked against the cache."""
+    n, heads, dim = shape
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
+        raise TypeError("codes must be uint8 and scales float32")
+    if codes.shape != (n, heads, dim >> 1 if fmt == GPTQ_CACHE_INT4 else dim) \
+            or not codes.is_contiguous():
+        raise ValueError("codes must be contiguous, n_slots x heads x bytes of a head")
+    if scales.shape != (n, heads, groups) or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous, n_slots x heads x groups")
+    if fmt == GPTQ_CACHE_E4M3:
+        return codes.data_ptr(), scales.data_ptr(), None
+    if zeros.dtype is not torch.uint8:
+        raise TypeError("zeros must be uint8")
+    if zeros.shape != scales.shape or not zeros.is_contiguous():
+        raise ValueError("zeros must be contiguous and have the shape of scales")
+    return codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()
 
 
-def _cache_values(K, V, slots):
-    """(tokens, heads, head_dim) and the strides of K and V (tokens x heads x head_dim, the last
-    axis contiguous)."""
-    _typed(slots, torch.int64, "slots")
+_NO_PLANE = (None, None, None)
+
+
+def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_v, scales_v, zeros_v):
+    """Checks what both cache calls take. Returns (device, slots of the cache, (tokens, heads,
+    head_dim), address and strides of K, of V, addresses of the cache's arrays)."""
     t, h, d = K.shape
-    _want(slots.shape == (t,) and slots.is_contiguous(), "slots must be one number per token")
-    _want(d < 2 or K.stride(2) == 1, "K: the values of a head must be contiguous")
-    if V is not None:
-        _want(V.shape == K.shape, "V must have the shape of K")
-        _typed(V, K.dtype, "V")
-        _want(d < 2 or V.stride(2) == 1, "V: the values of a head must be contiguous")
-        return t, h, d, K.stride(0), K.stride(1), V.data_ptr(), V.stride(0), V.stride(1)
-    return t, h, d, K.stride(0), K.stride(1), None, 0, 0
+    _typed(slots, torch.int64, "slots")
+    if slots.shape != (t,) or not slots.is_contiguous():
+        raise ValueError("slots must be one number per token")
+    kt, kh, one = K.stride()
+    if one != 1 and d > 1:
+        raise ValueError("K: the values of a head must be contiguous")
+    n = codes_k.shape[0]
+    if group_size < 0 or (group_size and d % group_size):
+        raise ValueError("group_size must divide head_dim")
+    groups = d // group_size if group_size else 1
+    pk = _cache_plane((n, h, d), fmt, groups, codes_k, scales_k, zeros_k)
+    dev = K.get_device()
+    _same_device(dev, slots, codes_k, scales_k, zeros_k)
+    if V is None:
+        return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (None, 0, 0), pk + _NO_PLANE
+    if V.shape != K.shape:
+        raise ValueError("V must have the shape of K")
+    _typed(V, K.dtype, "V")
+    vt, vh, one = V.stride()
+    if one != 1 and d > 1:
+        raise ValueError("V: the values of a head must be contiguous")
+    pv = _cache_plane((n, h, d), fmt, groups, codes_v, scales_v, zeros_v)
+    _same_device(dev, V, codes_v, scales_v, zeros_v)
+    return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (V.data_ptr(), vt, vh), pk + pv
 
 
 def gptq_cache_write(K: torch.Tensor, V: torch.Tensor | None, slots: torch.Tensor, fmt: int,
@@ -200,19 +230,19 @@ def gptq_cache_write(K: torch.Tensor, V: torch.Tensor | None, slots: torch.Tenso
                      claims: torch.Tensor | None, stream=None):
     """Quantize rows of K and V (tokens x heads x head_dim) into ``slots`` of a cache. Negative
     slots skip their token; of tokens with the same slot the last one stays."""
-    t, h, d, ks, kh, vp, vs, vh = _cache_values(K, V, slots)
-    n = codes_k.shape[0]
-    p = _cache_arrays(n, h, d, fmt, group_size, (codes_k, scales_k, zeros_k, codes_v, scales_v,
-                                                 zeros_v), V is not None)
+    dev, n, thd, k, v, planes = _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k,
+                                            codes_v, scales_v, zeros_v)
+    cp = None
     if claims is not None:
         _typed(claims, torch.int32, "claims")
-        _want(claims.shape == (n,) and claims.is_contiguous(), "claims must be one number per slot")
-    on = [x for x in (K, V, slots, codes_k, scales_k, zeros_k, codes_v, scales_v, zeros_v, claims)
-          if x is not None]
-    st = _stream_of(stream, on)
-    _check(_cache_write(K.data_ptr(), ks, kh, vp, vs, vh, _code(K), t, h, d, slots.data_ptr(), n, fmt,
-                        group_size, *p, None if claims is None else claims.data_ptr(), st),
-           "gptq_cache_write")
+        if claims.shape != (n,) or not claims.is_contiguous():
+            raise ValueError("claims must be one number per slot")
+        _same_device(dev, claims)
+        cp = claims.data_ptr()
+    st = _cache_write(*k, *v, _code(K), *thd, slots.data_ptr(), n, fmt, group_size, *planes, cp,
+                      _stream_of(stream, dev))
+    if st:
+        raise GptqError(st, "gptq_cache_write")
 
 
 def gptq_cache_read(slots: torch.Tensor, fmt: int, group_size: int, codes_k: torch.Tensor,
@@ -222,15 +252,12 @@ def gptq_cache_read(slots: torch.Tensor, fmt: int, group_size: int, codes_k: tor
                     stream=None):
     """K, V (tokens x heads x head_dim, written) = the values of the cache's ``slots``. Rows of
     negative slots are left as they are."""
-    t, h, d, ks, kh, vp, vs, vh = _cache_values(K, V, slots)
-    n = codes_k.shape[0]
-    p = _cache_arrays(n, h, d, fmt, group_size, (codes_k, scales_k, zeros_k, codes_v, scales_v,
-                                                 zeros_v), V is not None)
-    on = [x for x in (K, V, slots, codes_k, scales_k, zeros_k, codes_v, scales_v, zeros_v)
-          if x is not None]
-    st = _stream_of(stream, on)
-    _check(_cache_read(slots.data_ptr(), t, n, h, d, fmt, group_size, *p, K.data_ptr(), ks, kh, vp,
-                       vs, vh, _code(K), st), "gptq_cache_read")
+    dev, n, (t, h, d), k, v, planes = _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k,
+                                                  zeros_k, codes_v, scales_v, zeros_v)
+    st = _cache_read(slots.data_ptr(), t, n, h, d, fmt, group_size, *planes, *k, *v, _code(K),
+                     _stream_of(stream, dev))
+    if st:
+        raise GptqError(st, "gptq_cache_read")
 
 
 def kv_cache(n_slots: int, heads: int, head_dim: int, *, fmt: int = GPTQ_CACHE_INT8,

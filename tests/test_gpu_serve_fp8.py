@@ -277,3 +277,17 @@ def test_a_captured_step_follows_its_inputs(g):
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
     g.gptq_sync_status()
+
+
+@pytest.mark.parametrize("n,dtype", [(2816, "bf16"), (2816, "fp32"), (2801, "bf16"), (2801, "fp16"),
+                                     (2802, "bf16"), (2801, "fp32"), (2630, "bf16"), (2624, "fp16")])
+def test_matmul_rows_of_any_alignment_at_large_sizes(g, n, dtype):
+    """The large-size kernel's stores: whole boxes, ragged last boxes, rows that start between two
+    32-bit words. Two sampled row blocks, and every column of them."""
+    m, k = 3000, 300
+    A, sA, B, sB = operands(g, m, n, k)
+    Y = g.fp8_matmul(A, sA, B, sB, out_dtype=DT[dtype])
+    g.gptq_sync_status()
+    at = torch.cat([torch.arange(0, 40), torch.arange(1270, 1300), torch.arange(2960, 3000)]).to(DEV)
+    judge(Y[at], A.view(torch.uint8)[at].view(F8), sA[at], B, sB, dtype)
+    assert torch.isfinite(Y).all()
