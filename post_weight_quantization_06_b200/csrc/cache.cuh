@@ -1,8 +1,7 @@
 // The quantized cache of keys and values (gptq_cache_write, gptq_cache_read).
 //
 // Write: a unit is one group of one head of one token of K or V. A power of two of lanes holds
-// it, eight values each (up to four times eight for groups above 256), between its range and its
-// codes: one pass over the values. Read: a unit is eight values.
+// it, up to 32 values each, between its range and its codes: one pass over the values. Read: a unit is eight values.
 //   int:  s = max((mx - mn) / maxq, 2^-126), z = rint(-mn maxq / (mx - mn)),
 //         c = clamp(rint(x / s + z)), value s (c - z)
 //   e4m3: s = max(max |x| / 448, 2^-126), c = e4m3(x / s), value s c
@@ -95,12 +94,10 @@ constexpr float CACHE_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to a 
 
 // Min-max grid of a group: scale, its reciprocal, zero-point. The zero-point's quotient is
 // decided in fp64, where -mn maxq and mx - mn are exact: a symmetric range lies on the border
-// between two zero-points, and fp32 would pick either.
+// between two zero-points, and fp32 would pick either. False where the range is not finite.
 __device__ __forceinline__ bool cache_grid(float mn, float mx, float maxq, float &s, float &r,
                                            float &z) {
-    mn = fminf(mn, 0.f);
-    mx = fmaxf(mx, 0.f);
-    if (mx == mn) { mn = -1.f; mx = 1.f; }
+    if (mx == mn) { mn = -1.f; mx = 1.f; }   // both zero: the range starts from there
     const float range = mx - mn;
     if (!finitef(range)) return false;
     s = fmaxf(__fdiv_rn(range, maxq), SCALE_MIN);
@@ -115,7 +112,7 @@ __device__ __forceinline__ bool cache_grid(float mn, float mx, float maxq, float
     return true;
 }
 
-template <typename T, int FMT, int V>
+template <typename T, int FMT>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     __shared__ int beaten[CACHE_MAX_TB];
@@ -138,52 +135,46 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
         const long long sl = live ? slot[j] : -1;
         const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
                      (long long)h * p.hs + (long long)g * a.group;
-        Raw8<T> raw[V];
+        Raw8<T> raw[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int v = l + i * w;
             const bool on = sl >= 0 && v < nvec;
             load8(x + (on ? 8 * v : 0), on && p.vec, on ? 8 : 0, raw[i]);
         }
         float s, r, z = 0.f;
         bool bad;
-        uint32_t top = 0;
-        float mn = 0.f, mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float v[8];
-            widen8(raw[i], v);
-            top = max(top, amax_bits8(v));
-            if (FMT != GPTQ_CACHE_E4M3) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) { mn = fminf(mn, v[e]); mx = fmaxf(mx, v[e]); }
-            }
-        }
-        for (int o = w >> 1; o; o >>= 1) {
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (FMT != GPTQ_CACHE_E4M3) {
-                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            }
-        }
-        bad = top >= INF_BITS;
         if (FMT == GPTQ_CACHE_E4M3) {
-            if (__any_sync(0xffffffffu, bad)) {
-                top = 0;
+            Amax<T> am;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < 4; ++i) am.add(raw[i]);
+            float m = am.value();
+            for (int o = w >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            bad = !finitef(m);
+            if (__any_sync(0xffffffffu, bad)) {
+                m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     float v[8];
                     widen8(raw[i], v);
-                    top = max(top, amax_finite8(v));
+                    m = fmaxf(m, amax_finite8(v));
                 }
-                for (int o = w >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int o = w >> 1; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             }
-            s = e4m3_scale(top);
+            s = e4m3_scale(m);
             r = __frcp_rn(s);
         } else {
             constexpr float maxq = FMT == GPTQ_CACHE_INT4 ? 15.f : 255.f;
-            if (bad || !cache_grid(mn, mx, maxq, s, r, z)) {
-                bad = true;
+            MinMax<T> mm;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mm.add(raw[i]);
+            float mn = mm.low(), mx = mm.high();
+            for (int o = w >> 1; o; o >>= 1) {
+                mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            }
+            bad = !cache_grid(mn, mx, maxq, s, r, z);
+            if (bad) {
                 s = __uint_as_float(0x7fffffffu);
                 r = 0.f;
                 z = 0.f;
@@ -199,7 +190,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
         }
         const long long at = row * a.dim + (long long)g * a.group;  // element of the first code
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int v = l + i * w;
             if (v >= nvec) continue;
             float f[8];
@@ -332,13 +323,11 @@ inline int cache_tokens_per_cta(int tokens) {
 
 template <typename T, int FMT>
 inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
-    const int nvec = a.group / 8;
+    // four vectors of eight a lane: what a group costs once (its grid) is shared by 32 values
     a.w = 1;
-    while (a.w < 32 && a.w < nvec) a.w *= 2;
+    while (4 * a.w < a.group / 8) a.w *= 2;
     const dim3 grid((a.tokens + a.tb - 1) / a.tb);
-    if (nvec <= a.w)
-        return launch_kernel(cache_write_kernel<T, FMT, 1>, grid, dim3(CACHE_THREADS), 0, s, true, a);
-    return launch_kernel(cache_write_kernel<T, FMT, 4>, grid, dim3(CACHE_THREADS), 0, s, true, a);
+    return launch_kernel(cache_write_kernel<T, FMT>, grid, dim3(CACHE_THREADS), 0, s, true, a);
 }
 template <typename T>
 inline int cache_write_fmt(CacheArgs &a, int format, cudaStream_t s) {

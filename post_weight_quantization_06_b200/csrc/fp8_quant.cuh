@@ -32,54 +32,60 @@ __device__ __forceinline__ void store_codes8(unsigned char *p, bool vec, int hav
 }
 
 constexpr int FQ_THREADS = 256;
-constexpr int FQ_UNITS = 4;  // units in flight per half warp
 
-// block_rows 1: a half warp per block, eight values per lane; each half warp takes FQ_UNITS
-// blocks, all loaded before the first is worked on.
+// block_rows 1: four lanes per block, 32 values each (16-byte pieces l, l + 4, ... of the block's
+// sixteen). The scale, its reciprocal and the block's place cost some 70 instructions, which at
+// 8 values a lane was more than all the rest: 16384 x 6144 bf16 in 88 us, with 32 in FQ_US us.
 template <typename T>
 __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_rows_kernel(Fp8QuantArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
-    const int lane = threadIdx.x & 31, l = lane & 15;
-    const long long half = ((long long)blockIdx.x * FQ_THREADS + threadIdx.x) >> 4;
-    const long long halves = (long long)gridDim.x * (FQ_THREADS / 16);
-    Raw8<T> raw[FQ_UNITS];
-    uint32_t row[FQ_UNITS], b[FQ_UNITS];
-    int have[FQ_UNITS];
+    const int l = threadIdx.x & 3;
+    const long long u = ((long long)blockIdx.x * FQ_THREADS + threadIdx.x) >> 2;
+    const bool live = u < a.units;
+    const uint32_t row = live ? (uint32_t)u / a.kb : 0, b = live ? (uint32_t)u - row * a.kb : 0;
+    const long long left = live ? a.cols - (long long)b * 128 : 0;   // columns of the block, at most
+    const T *x = static_cast<const T *>(a.X) + (long long)row * a.ldx + (long long)b * 128;
+    Raw8<T> raw[4];
 #pragma unroll
-    for (int i = 0; i < FQ_UNITS; ++i) {
-        const long long u = half + i * halves;
-        have[i] = -1;
-        row[i] = b[i] = 0;
-        if (u < a.units) {
-            row[i] = (uint32_t)u / a.kb;
-            b[i] = (uint32_t)u - row[i] * a.kb;
-            const long long c = (long long)b[i] * 128 + 8 * l;
-            have[i] = (int)max(0LL, min(8LL, a.cols - c));
-        }
-        const T *p = static_cast<const T *>(a.X) + (long long)row[i] * a.ldx + (long long)b[i] * 128 + 8 * l;
-        load8(p, a.vec_in && have[i] == 8, have[i], raw[i]);
+    for (int i = 0; i < 4; ++i) {
+        const int c = 8 * (l + 4 * i);
+        const int have = (int)max(0LL, min(8LL, left - c));
+        load8(have ? x + c : x, a.vec_in && have == 8, have, raw[i]);
     }
+    Amax<T> am;
 #pragma unroll
-    for (int i = 0; i < FQ_UNITS; ++i) {
+    for (int i = 0; i < 4; ++i) am.add(raw[i]);
+    float m = am.value();
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool bad = !finitef(m);
+    if (__any_sync(0xffffffffu, bad)) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[8];
+            widen8(raw[i], v);
+            m = fmaxf(m, amax_finite8(v));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (bad && l == 0) report(GPTQ_ERR_NONFINITE, row);
+    }
+    if (!live) return;
+    const float s = e4m3_scale(m), r = __frcp_rn(s);
+    if (l == 0) a.scales[(long long)row * a.kb + b] = s;
+    unsigned char *y = a.codes + (long long)row * a.ldc + (long long)b * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = 8 * (l + 4 * i);
+        const int have = (int)max(0LL, min(8LL, left - c));
+        if (!have) continue;
         float v[8];
         widen8(raw[i], v);
-        uint32_t m = amax_bits8(v);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (__any_sync(0xffffffffu, m >= INF_BITS)) {
-            const bool bad = m >= INF_BITS;
-            m = amax_finite8(v);
-#pragma unroll
-            for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (bad && l == 0 && have[i] >= 0) report(GPTQ_ERR_NONFINITE, row[i]);
-        }
-        const float s = e4m3_scale(m);
-        const uint2 c = e4m3_codes8(v, __frcp_rn(s));
-        if (have[i] < 0) continue;
-        if (l == 0) a.scales[(long long)row[i] * a.kb + b[i]] = s;
-        store_codes8(a.codes + (long long)row[i] * a.ldc + (long long)b[i] * 128 + 8 * l,
-                     a.vec_out && have[i] == 8, have[i], c);
+        // an infinity becomes the format's NaN: its product with r would saturate
+        if (bad) amax_finite8(v);
+        store_codes8(y + c, a.vec_out && have == 8, have, e4m3_codes8(v, r));
     }
 }
 
@@ -88,45 +94,47 @@ template <typename T>
 __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8QuantArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
-    __shared__ uint32_t wmax[2][FQ_THREADS / 32];
+    __shared__ float wmax[2][FQ_THREADS / 32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t br = blockIdx.x / a.kb, b = blockIdx.x - br * a.kb;
     const long long c = (long long)b * 128 + 8 * (t & 15);
     const int have = (int)max(0LL, min(8LL, a.cols - c));
     Raw8<T> raw[8];
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const long long r = (long long)br * 128 + (t >> 4) + 16 * i;
         const int n = r < a.rows ? have : 0;
         load8(static_cast<const T *>(a.X) + (n ? r * a.ldx + c : 0), a.vec_in && n == 8, n, raw[i]);
     }
+    Amax<T> am;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float v[8];
-        widen8(raw[i], v);
-        m = max(m, amax_bits8(v));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
+    for (int i = 0; i < 8; ++i) am.add(raw[i]);
+    float m = am.value();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) wmax[0][warp] = m;
     __syncthreads();
-    m = 0;
+    m = 0.f;
 #pragma unroll
-    for (int w = 0; w < FQ_THREADS / 32; ++w) m = max(m, wmax[0][w]);
-    if (m >= INF_BITS) {  // the same in every thread
-        m = 0;
+    for (int w = 0; w < FQ_THREADS / 32; ++w) m = max_nan(m, wmax[0][w]);
+    const bool bad = !finitef(m);   // the same in every thread
+    if (bad) {
+        m = 0.f;
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
             float v[8];
             widen8(raw[i], v);
-            if (amax_bits8(v) >= INF_BITS)
+            Amax<T> one;
+            one.add(raw[i]);
+            if (!finitef(one.value()))
                 report(GPTQ_ERR_NONFINITE, (long long)br * 128 + (t >> 4) + 16 * i);
-            m = max(m, amax_finite8(v));
+            m = fmaxf(m, amax_finite8(v));
         }
-        m = __reduce_max_sync(0xffffffffu, m);
+        m = warp_max(m);
         if (lane == 0) wmax[1][warp] = m;
         __syncthreads();
-        m = 0;
-        for (int w = 0; w < FQ_THREADS / 32; ++w) m = max(m, wmax[1][w]);
+        m = 0.f;
+        for (int w = 0; w < FQ_THREADS / 32; ++w) m = fmaxf(m, wmax[1][w]);
     }
     const float s = e4m3_scale(m), r = __frcp_rn(s);
     if (t == 0) a.scales[blockIdx.x] = s;
@@ -136,8 +144,7 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8Quant
         if (row >= a.rows || have == 0) continue;
         float v[8];
         widen8(raw[i], v);
-        // an infinity becomes the format's NaN: its product with r would saturate
-        if (amax_bits8(v) >= INF_BITS) amax_finite8(v);
+        if (bad) amax_finite8(v);
         store_codes8(a.codes + row * a.ldc + c, a.vec_out && have == 8, have, e4m3_codes8(v, r));
     }
 }
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8Quant
 template <typename T>
 inline int fp8_quantize_launch(const Fp8QuantArgs &a, int block_rows, cudaStream_t s) {
     if (block_rows == 1) {
-        const long long per = FQ_THREADS / 16 * FQ_UNITS;
+        const long long per = FQ_THREADS / 4;
         return launch_kernel(fp8_quantize_rows_kernel<T>, dim3((unsigned)((a.units + per - 1) / per)),
                              dim3(FQ_THREADS), 0, s, true, a);
     }

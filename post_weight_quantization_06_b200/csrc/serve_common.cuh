@@ -12,7 +12,6 @@ namespace serve {
 
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126: a scale and its reciprocal stay normal
-constexpr uint32_t INF_BITS = 0x7f800000u;
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -67,28 +66,97 @@ __device__ __forceinline__ void store8(T *p, bool vec, const float *v) {
     }
 }
 
-// Largest |v| as fp32 bits: these order like the values, NaN above infinity above the rest, so
-// one maximum also tells whether all eight are finite.
-__device__ __forceinline__ uint32_t amax_bits8(const float *v) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
-    return a;
+// Maximum and minimum that let a NaN through: whether a group is finite is then seen from its
+// range, without a test per value.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
-// The finite ones' largest; the others become NaN. Rare.
-__device__ __forceinline__ uint32_t amax_finite8(float *v) {
-    uint32_t a = 0;
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// Largest |x|, and smallest and largest x, of vectors of eight; 16-bit types two at a time.
+template <typename T>
+struct Amax {
+    float m = 0.f;
+    __device__ __forceinline__ void add(const Raw8<T> &r) {
+        const T *e = reinterpret_cast<const T *>(r.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(e[i]));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+};
+template <typename T>
+struct MinMax {
+    float mn = 0.f, mx = 0.f;
+    __device__ __forceinline__ void add(const Raw8<T> &r) {
+        const T *e = reinterpret_cast<const T *>(r.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            mn = min_nan(mn, e[i]);
+            mx = max_nan(mx, e[i]);
+        }
+    }
+    __device__ __forceinline__ float low() const { return mn; }
+    __device__ __forceinline__ float high() const { return mx; }
+};
+#define SERVE_PACKED_RANGE(T, T2)                                                            \
+    template <>                                                                              \
+    struct Amax<T> {                                                                         \
+        uint32_t m = 0;                                                                      \
+        __device__ __forceinline__ void add(const Raw8<T> &r) {                              \
+            const T2 *e = reinterpret_cast<const T2 *>(r.w);                                 \
+            T2 t = *reinterpret_cast<T2 *>(&m);                                              \
+            _Pragma("unroll") for (int i = 0; i < 4; ++i) t = __hmax2_nan(t, __habs2(e[i])); \
+            m = *reinterpret_cast<uint32_t *>(&t);                                           \
+        }                                                                                    \
+        __device__ __forceinline__ float value() const {                                     \
+            const T2 t = *reinterpret_cast<const T2 *>(&m);                                  \
+            return max_nan(widen(t.x), widen(t.y));                                          \
+        }                                                                                    \
+    };                                                                                       \
+    template <>                                                                              \
+    struct MinMax<T> {                                                                       \
+        uint32_t mn = 0, mx = 0;                                                             \
+        __device__ __forceinline__ void add(const Raw8<T> &r) {                              \
+            const T2 *e = reinterpret_cast<const T2 *>(r.w);                                 \
+            T2 a = *reinterpret_cast<T2 *>(&mn), b = *reinterpret_cast<T2 *>(&mx);           \
+            _Pragma("unroll") for (int i = 0; i < 4; ++i) {                                  \
+                a = __hmin2_nan(a, e[i]);                                                    \
+                b = __hmax2_nan(b, e[i]);                                                    \
+            }                                                                                \
+            mn = *reinterpret_cast<uint32_t *>(&a);                                          \
+            mx = *reinterpret_cast<uint32_t *>(&b);                                          \
+        }                                                                                    \
+        __device__ __forceinline__ float low() const {                                       \
+            const T2 t = *reinterpret_cast<const T2 *>(&mn);                                 \
+            return min_nan(widen(t.x), widen(t.y));                                          \
+        }                                                                                    \
+        __device__ __forceinline__ float high() const {                                      \
+            const T2 t = *reinterpret_cast<const T2 *>(&mx);                                 \
+            return max_nan(widen(t.x), widen(t.y));                                          \
+        }                                                                                    \
+    };
+SERVE_PACKED_RANGE(__nv_bfloat16, __nv_bfloat162)
+SERVE_PACKED_RANGE(__half, __half2)
+#undef SERVE_PACKED_RANGE
+
+// The largest of the finite |v|; the others become NaN. For groups that are not finite.
+__device__ __forceinline__ float amax_finite8(float *v) {
+    float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-        if (b >= INF_BITS) v[i] = __uint_as_float(0x7fffffffu);
-        else a = max(a, b);
+        if (!finitef(v[i])) v[i] = __uint_as_float(0x7fffffffu);
+        else a = fmaxf(a, fabsf(v[i]));
     }
     return a;
 }
 
-__device__ __forceinline__ float e4m3_scale(uint32_t amax) {
-    return fmaxf(__fdiv_rn(__uint_as_float(amax), E4M3_MAX), SCALE_MIN);
+__device__ __forceinline__ float e4m3_scale(float amax) {
+    return fmaxf(__fdiv_rn(amax, E4M3_MAX), SCALE_MIN);
 }
 
 // x r truncated to fp32 with the last bit set where the truncation dropped something: rounding
