@@ -9,6 +9,8 @@
 // decode step; a CTA takes a few whole tokens, so that the slots are looked at once per token.
 #pragma once
 
+#include <algorithm>
+
 #include "serve_common.cuh"
 
 namespace gptq {
@@ -25,7 +27,7 @@ struct CachePlane {
     unsigned char *codes;
     float *scales;
     uint8_t *zeros;
-    int vec;               // x or y takes 16-byte accesses
+    int vec;               // x or y takes 16-byte (1) or 32-byte (2) accesses
 };
 
 struct CacheArgs {
@@ -37,6 +39,7 @@ struct CacheArgs {
     int tb;                         // tokens of a CTA
     FastDiv per_token, per_plane, per_head, per_group;  // units (see each kernel)
     int w;                          // lanes of a unit (write)
+    int vec;                        // codes take 16-byte accesses (read)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -112,6 +115,34 @@ __device__ __forceinline__ bool cache_grid(float mn, float mx, float maxq, float
     return true;
 }
 
+// Where a unit's values are, and what it is.
+struct WriteUnit {
+    uint32_t j, pl, h, g;
+    bool live;
+    __device__ __forceinline__ void place(const CacheArgs &a, uint32_t u, uint32_t units) {
+        live = u < units;
+        if (!live) u = 0;
+        j = a.per_token.div(u);
+        const uint32_t rem = u - j * a.per_token.d;
+        pl = a.per_plane.div(rem);
+        const uint32_t hg = rem - pl * a.per_plane.d;
+        h = a.per_head.div(hg);
+        g = hg - h * a.per_head.d;
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const CacheArgs &a, int t0, int l, int nvec, Raw8<T> *raw) const {
+        const CachePlane &p = a.p[pl];
+        const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
+                     (long long)h * p.hs + (long long)g * a.group;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = l + i * a.w;
+            const bool on = live && v < nvec;
+            load8(x + (on ? 8 * v : 0), on && p.vec, on ? 8 : 0, raw[i]);
+        }
+    }
+};
+
 template <typename T, int FMT>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
@@ -124,24 +155,20 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
     const uint32_t units = (uint32_t)nt * a.per_token.d;
     const uint32_t step = CACHE_THREADS / w;
     const int nvec = a.group >> 3;
+    // the first values are on their way while the slots are looked at
+    WriteUnit at0;
+    Raw8<T> raw[4];
+    at0.place(a, threadIdx.x / w, units);
+    at0.load(a, t0, l, nvec, raw);
     cache_resolve(a, t0, nt, slot, beaten);
     for (uint32_t u0 = 0; u0 < units; u0 += step) {
-        const uint32_t u = u0 + threadIdx.x / w;
-        const bool live = u < units;
-        const uint32_t j = a.per_token.div(live ? u : 0), rem = live ? u - j * a.per_token.d : 0;
-        const uint32_t pl = a.per_plane.div(rem), hg = rem - pl * a.per_plane.d;
-        const uint32_t h = a.per_head.div(hg), g = hg - h * a.per_head.d;
-        const CachePlane &p = a.p[pl];
-        const long long sl = live ? slot[j] : -1;
-        const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
-                     (long long)h * p.hs + (long long)g * a.group;
-        Raw8<T> raw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = l + i * w;
-            const bool on = sl >= 0 && v < nvec;
-            load8(x + (on ? 8 * v : 0), on && p.vec, on ? 8 : 0, raw[i]);
+        if (u0) {
+            at0.place(a, u0 + threadIdx.x / w, units);
+            at0.load(a, t0, l, nvec, raw);
         }
+        const uint32_t j = at0.j, h = at0.h, g = at0.g;
+        const CachePlane &p = a.p[at0.pl];
+        const long long sl = at0.live ? slot[j] : -1;
         float s, r, z = 0.f;
         bool bad;
         if (FMT == GPTQ_CACHE_E4M3) {
@@ -215,10 +242,11 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
                                                     __byte_perm(c[6], c[7], 0x0040), 0x5410);
                     *reinterpret_cast<uint2 *>(p.codes + at + 8 * v) = make_uint2(lo, hi);
                 } else {
-                    uint32_t word = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) word |= (c[e] & 15u) << (4 * e);
-                    *reinterpret_cast<uint32_t *>(p.codes + (at >> 1) + 4 * v) = word;
+                    // the low byte of c0 + 16 c1 is both codes: the bits above them in c0 and c1
+                    // (2^23's) lie beyond it
+                    const uint32_t lo = __byte_perm(c[0] + 16 * c[1], c[2] + 16 * c[3], 0x0040);
+                    const uint32_t hi = __byte_perm(c[4] + 16 * c[5], c[6] + 16 * c[7], 0x0040);
+                    *reinterpret_cast<uint32_t *>(p.codes + (at >> 1) + 4 * v) = __byte_perm(lo, hi, 0x5410);
                 }
             }
         }
@@ -230,9 +258,42 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
 // ---------------------------------------------------------------------------------------
 constexpr int CACHE_READ_UNROLL = 4;
 
-// One unit is eight values; per_token.d units per token over the planes, per_plane.d per plane,
-// per_head.d per head, and per_group.d of them share a scale.
-template <typename T, int FMT>
+__device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+// Eight values of one word (4 bits) or two (8 bits).
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 c, float s, float z, float *f) {
+    if (FMT == GPTQ_CACHE_E4M3) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = e < 2 ? c.x : c.y;
+            uint32_t h2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * (e & 1)))));
+            const __half2 hv = *reinterpret_cast<const __half2 *>(&h2);
+            f[2 * e] = __low2float(hv) * s;
+            f[2 * e + 1] = __high2float(hv) * s;
+        }
+    } else {
+        // a code in the low bits of 2^23 is 2^23 + code: the difference is exact
+        const float bias = 8388608.f + z;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t q;
+            if (FMT == GPTQ_CACHE_INT4) q = ((c.x >> (4 * e)) & 15u) | 0x4b000000u;
+            else q = __byte_perm(e < 4 ? c.x : c.y, 0x4b000000u, 0x7440u | (e & 3));
+            f[e] = (__uint_as_float(q) - bias) * s;
+        }
+    }
+}
+
+// One unit is 8 U values; per_token.d units per token over the planes, per_plane.d per plane,
+// per_head.d per head, and per_group.d of them share a scale. U = 2 where heads and groups are
+// multiples of 16: what a unit's place costs is then shared by 16 values, and its 16-bit output
+// is one 32-byte store.
+template <typename T, int FMT, int U>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     pdl_launch_next();
@@ -249,19 +310,16 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_
     }
     __syncthreads();
     const uint32_t units = (uint32_t)nt * a.per_token.d;
-    const int groups = a.dim / a.group;
+    const int row = a.heads * a.dim, meta = a.heads * (a.dim / a.group);
     for (uint32_t u0 = threadIdx.x; u0 < units; u0 += CACHE_THREADS * CACHE_READ_UNROLL) {
-        uint2 c[CACHE_READ_UNROLL];
+        uint2 c[CACHE_READ_UNROLL][U];
         float s[CACHE_READ_UNROLL], z[CACHE_READ_UNROLL];
         T *y[CACHE_READ_UNROLL];
-        bool vec[CACHE_READ_UNROLL];
+        int vec[CACHE_READ_UNROLL];
 #pragma unroll
         for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
             const uint32_t u = u0 + i * CACHE_THREADS;
             y[i] = nullptr;
-            vec[i] = false;
-            c[i] = make_uint2(0, 0);
-            s[i] = z[i] = 0.f;
             if (u >= units) continue;
             const uint32_t j = a.per_token.div(u), rem = u - j * a.per_token.d;
             const long long sl = slot[j];
@@ -269,44 +327,46 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_
             const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d;
             const CachePlane &p = a.p[pl];
             const uint32_t h = a.per_head.div(v);
-            const long long at = sl * a.heads * a.dim + 8LL * v;
-            const long long m = sl * a.heads * groups + a.per_group.div(v);
-            if (FMT == GPTQ_CACHE_INT4)
-                c[i].x = *reinterpret_cast<const uint32_t *>(p.codes + (at >> 1));
-            else
-                c[i] = *reinterpret_cast<const uint2 *>(p.codes + at);
+            const long long at = sl * row + 8LL * U * v;
+            if (FMT == GPTQ_CACHE_INT4) {
+                if (U == 2) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(p.codes + (at >> 1));
+                    c[i][0].x = q.x;
+                    c[i][U - 1].x = q.y;
+                } else {
+                    c[i][0].x = *reinterpret_cast<const uint32_t *>(p.codes + (at >> 1));
+                }
+            } else if (U == 2 && a.vec) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(p.codes + at);
+                c[i][0] = make_uint2(q.x, q.y);
+                c[i][U - 1] = make_uint2(q.z, q.w);
+            } else {
+#pragma unroll
+                for (int k = 0; k < U; ++k) c[i][k] = *reinterpret_cast<const uint2 *>(p.codes + at + 8 * k);
+            }
+            const long long m = sl * meta + a.per_group.div(v);
             s[i] = p.scales[m];
-            if (FMT != GPTQ_CACHE_E4M3) z[i] = (float)p.zeros[m];
+            z[i] = FMT != GPTQ_CACHE_E4M3 ? (float)p.zeros[m] : 0.f;
             y[i] = static_cast<T *>(p.y) + (long long)(t0 + (int)j) * p.ts + (long long)h * p.hs +
-                   8LL * (v - h * a.per_head.d);
+                   8 * U * (v - h * a.per_head.d);
             vec[i] = p.vec;
         }
 #pragma unroll
         for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
             if (!y[i]) continue;
-            float f[8];
-            if (FMT == GPTQ_CACHE_E4M3) {
+            float f[8 * U];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w = e < 2 ? c[i].x : c[i].y;
-                    uint32_t h2;
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * (e & 1)))));
-                    const __half2 hv = *reinterpret_cast<const __half2 *>(&h2);
-                    f[2 * e] = __low2float(hv) * s[i];
-                    f[2 * e + 1] = __high2float(hv) * s[i];
-                }
+            for (int k = 0; k < U; ++k) decode8<FMT>(c[i][k], s[i], z[i], f + 8 * k);
+            if (U == 2 && sizeof(T) == 2 && vec[i] == 2) {
+                uint4 o[2];
+                T *e = reinterpret_cast<T *>(o);
+#pragma unroll
+                for (int k = 0; k < 8 * U; ++k) e[k & 15] = narrow<T>(f[k]);
+                store32(y[i], o[0], o[1]);
             } else {
-                // a code in the low bits of 2^23 is 2^23 + code: the difference is exact
-                const float bias = 8388608.f + z[i];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    uint32_t q;
-                    if (FMT == GPTQ_CACHE_INT4) q = ((c[i].x >> (4 * e)) & 15u) | 0x4b000000u;
-                    else q = __byte_perm(e < 4 ? c[i].x : c[i].y, 0x4b000000u, 0x7440u | (e & 3));
-                    f[e] = (__uint_as_float(q) - bias) * s[i];
-                }
+                for (int k = 0; k < U; ++k) store8(y[i] + 8 * k, vec[i] != 0, f + 8 * k);
             }
-            store8(y[i], vec[i], f);
         }
     }
 }
@@ -314,11 +374,12 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_
 // ---------------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------------
-inline int cache_tokens_per_cta(int tokens) {
-    // enough CTAs for several per SM before a CTA takes more than one token
-    const int want = device_sm_count() * 8;
-    int tb = tokens / want;
-    return tb < 1 ? 1 : tb > CACHE_MAX_TB ? CACHE_MAX_TB : tb;
+// Tokens of a CTA: as many as its threads take at once (`per_token` threads each), more where that
+// leaves several CTAs per SM all the same.
+inline int cache_tokens_per_cta(int tokens, long long per_token) {
+    const int once = (int)std::max(1LL, std::min<long long>(CACHE_MAX_TB, CACHE_THREADS / per_token));
+    const int most = tokens / (device_sm_count() * 8) / once * once;
+    return std::min(CACHE_MAX_TB, std::max(once, most));
 }
 
 template <typename T, int FMT>
@@ -326,6 +387,7 @@ inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
     // four vectors of eight a lane: what a group costs once (its grid) is shared by 32 values
     a.w = 1;
     while (4 * a.w < a.group / 8) a.w *= 2;
+    a.tb = cache_tokens_per_cta(a.tokens, (long long)a.per_token.d * a.w);
     const dim3 grid((a.tokens + a.tb - 1) / a.tb);
     return launch_kernel(cache_write_kernel<T, FMT>, grid, dim3(CACHE_THREADS), 0, s, true, a);
 }
@@ -343,7 +405,6 @@ inline int cache_write(CacheArgs &a, int x_dtype, int format, cudaStream_t s) {
     a.per_plane = fast_div((uint32_t)a.heads * groups);
     a.per_token = fast_div((uint32_t)planes * a.heads * groups);
     a.per_group = fast_div(1);
-    a.tb = cache_tokens_per_cta(a.tokens);
     if (a.tokens > GPTQ_CACHE_UNCLAIMED) {
         if (int st = launch_kernel(cache_claim_kernel, dim3((a.tokens + 255) / 256), dim3(256), 0, s,
                                    true, a.slots, a.tokens, a.n_slots, a.claims))
@@ -358,28 +419,38 @@ inline int cache_write(CacheArgs &a, int x_dtype, int format, cudaStream_t s) {
     }
 }
 
-template <typename T>
+template <typename T, int U>
 inline int cache_read_fmt(CacheArgs &a, int format, cudaStream_t s) {
     const dim3 grid((a.tokens + a.tb - 1) / a.tb), block(CACHE_THREADS);
     switch (format) {
-        case GPTQ_CACHE_INT4: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT4>, grid, block, 0, s, true, a);
-        case GPTQ_CACHE_INT8: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT8>, grid, block, 0, s, true, a);
-        default: return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_E4M3>, grid, block, 0, s, true, a);
+        case GPTQ_CACHE_INT4:
+            return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT4, U>, grid, block, 0, s, true, a);
+        case GPTQ_CACHE_INT8:
+            return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_INT8, U>, grid, block, 0, s, true, a);
+        default:
+            return launch_kernel(cache_read_kernel<T, GPTQ_CACHE_E4M3, U>, grid, block, 0, s, true, a);
     }
+}
+template <typename T>
+inline int cache_read_type(CacheArgs &a, int format, int unit, cudaStream_t s) {
+    return unit == 2 ? cache_read_fmt<T, 2>(a, format, s) : cache_read_fmt<T, 1>(a, format, s);
 }
 inline int cache_read(CacheArgs &a, int y_dtype, int format, cudaStream_t s) {
     const int planes = a.p[1].y ? 2 : 1;
-    a.per_head = fast_div(a.dim / 8);
-    a.per_plane = fast_div((uint32_t)a.heads * (a.dim / 8));
-    a.per_token = fast_div((uint32_t)planes * a.heads * (a.dim / 8));
-    a.per_group = fast_div(a.group / 8);
-    a.tb = cache_tokens_per_cta(a.tokens);
+    const int unit = a.dim % 16 == 0 && a.group % 16 == 0 ? 2 : 1;
+    a.per_head = fast_div(a.dim / (8 * unit));
+    a.per_plane = fast_div((uint32_t)a.heads * (a.dim / (8 * unit)));
+    a.per_token = fast_div((uint32_t)planes * a.heads * (a.dim / (8 * unit)));
+    a.per_group = fast_div(a.group / (8 * unit));
+    a.tb = cache_tokens_per_cta(a.tokens, (a.per_token.d + CACHE_READ_UNROLL - 1) / CACHE_READ_UNROLL);
     a.claims = nullptr;
     a.w = 1;
+    // 16 codes at once
+    a.vec = ((reinterpret_cast<uintptr_t>(a.p[0].codes) | reinterpret_cast<uintptr_t>(a.p[1].codes)) & 15u) == 0;
     switch (y_dtype) {
-        case GPTQ_BF16: return cache_read_fmt<__nv_bfloat16>(a, format, s);
-        case GPTQ_F16: return cache_read_fmt<__half>(a, format, s);
-        default: return cache_read_fmt<float>(a, format, s);
+        case GPTQ_BF16: return cache_read_type<__nv_bfloat16>(a, format, unit, s);
+        case GPTQ_F16: return cache_read_type<__half>(a, format, unit, s);
+        default: return cache_read_type<float>(a, format, unit, s);
     }
 }
 

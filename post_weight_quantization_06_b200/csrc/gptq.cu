@@ -891,9 +891,11 @@ static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, i
     if (heads == 1) return ts >= dim;
     return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
 }
+// How wide accesses to rows of x may be: 0 one value, 1 16 bytes, 2 32 bytes.
 static int cache_vec(const void *x, int64_t ts, int64_t hs, int dtype) {
-    const int64_t per = 16 / serve::serve_dtype_bytes(dtype);
-    return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ts % per == 0 && hs % per == 0;
+    const int64_t size = serve::serve_dtype_bytes(dtype);
+    const uint64_t all = reinterpret_cast<uintptr_t>(x) | (uint64_t)(ts * size) | (uint64_t)(hs * size);
+    return all % 32 == 0 ? 2 : all % 16 == 0 ? 1 : 0;
 }
 
 static int gptq_cache_write_body(const void *K, int64_t k_token_stride, int64_t k_head_stride,
