@@ -10,6 +10,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "serve_common.cuh"
 
@@ -40,6 +41,7 @@ struct CacheArgs {
     FastDiv per_token, per_plane, per_head, per_group;  // units (see each kernel)
     int w;                          // lanes of a unit (write)
     int vec;                        // codes take 16-byte accesses (read)
+    int full;                       // every lane has four vectors, all aligned (write)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -95,23 +97,47 @@ __device__ __forceinline__ void cache_resolve(const CacheArgs &a, int t0, int nt
 // ---------------------------------------------------------------------------------------
 constexpr float CACHE_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
 
-// Min-max grid of a group: scale, its reciprocal, zero-point. The zero-point's quotient is
-// decided in fp64, where -mn maxq and mx - mn are exact: a symmetric range lies on the border
-// between two zero-points, and fp32 would pick either. False where the range is not finite.
+// The whole number nearest to -mn maxq / (mx - mn), ties to even: a symmetric range lies on the
+// border between two, and rounded operands would pick either. In fp64 both products and the
+// difference are exact; the quotient's whole number is corrected by the remainder.
+__device__ __forceinline__ float cache_zero(float mn, float mx, float maxq, double) {
+    const double num = -(double)mn * (double)maxq, den = (double)mx - (double)mn;
+    int q = (int)rintf(__fdiv_rn(-mn, mx - mn) * maxq);
+    const double d = 2.0 * (num - (double)q * den);
+    if (d > den || (d == den && (q & 1))) ++q;
+    else if (d < -den || (d == -den && (q & 1))) --q;
+    return (float)min(max(q, 0), (int)maxq);
+}
+// The same in fp32 for values of 16-bit types (at most 11 bits): the product has 19, and the
+// difference is exact unless the exponents are 13 or more apart, where the quotient is far from
+// a border. A power of two keeps the product from overflowing. A quotient that rounds to a border
+// is decided by the sign of the remainder.
+__device__ __forceinline__ float cache_zero(float mn, float mx, float maxq, float) {
+    const float k = mx - mn > 1.f ? 0.00390625f : 1.f;
+    const float num = -mn * k * maxq, den = (mx - mn) * k;
+    const float q = __fdiv_rn(num, den);
+    float z = rintf(q);
+    if (fabsf(q - z) == 0.5f) {
+        const float r = fmaf(-q, den, num);
+        if (r != 0.f) z = q + (r > 0.f ? 0.5f : -0.5f);
+    }
+    return fminf(fmaxf(z, 0.f), maxq);
+}
+
+// Min-max grid of a group: scale, its reciprocal, zero-point. `edge`: an end of the range lies so
+// near the middle between a code and one that does not exist that codes have to be clamped.
+// False where the range is not finite.
+template <typename T>
 __device__ __forceinline__ bool cache_grid(float mn, float mx, float maxq, float &s, float &r,
-                                           float &z) {
+                                           float &z, bool &edge) {
     if (mx == mn) { mn = -1.f; mx = 1.f; }   // both zero: the range starts from there
     const float range = mx - mn;
     if (!finitef(range)) return false;
     s = fmaxf(__fdiv_rn(range, maxq), SCALE_MIN);
     r = __frcp_rn(s);
-    const double num = -(double)mn * (double)maxq, den = (double)mx - (double)mn;
-    // near the quotient, then the nearest by the remainder, ties to even
-    int q = (int)rintf(__fdiv_rn(-mn, range) * maxq);
-    const double d = 2.0 * (num - (double)q * den);
-    if (d > den || (d == den && (q & 1))) ++q;
-    else if (d < -den || (d == -den && (q & 1))) --q;
-    z = (float)min(max(q, 0), (int)maxq);
+    typedef typename std::conditional<sizeof(T) == 2, float, double>::type Z;
+    z = cache_zero(mn, mx, maxq, Z());
+    edge = fabsf(fmaf(mn, r, z)) > 0.499f || fabsf(fmaf(mx, r, z - maxq)) > 0.499f;
     return true;
 }
 
@@ -134,6 +160,12 @@ struct WriteUnit {
         const CachePlane &p = a.p[pl];
         const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
                      (long long)h * p.hs + (long long)g * a.group;
+        if (a.full) {   // units that do not exist read the first token's
+            x += 8 * l;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load8(x + i * 8 * a.w, true, 8, raw[i]);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int v = l + i * a.w;
@@ -144,7 +176,7 @@ struct WriteUnit {
 };
 
 template <typename T, int FMT>
-__global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? 6 : 4) cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     __shared__ int beaten[CACHE_MAX_TB];
     pdl_launch_next();
@@ -170,7 +202,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
         const CachePlane &p = a.p[at0.pl];
         const long long sl = at0.live ? slot[j] : -1;
         float s, r, z = 0.f;
-        bool bad;
+        bool bad, edge = false;
         if (FMT == GPTQ_CACHE_E4M3) {
             Amax<T> am;
 #pragma unroll
@@ -200,7 +232,8 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
                 mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
                 mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             }
-            bad = !cache_grid(mn, mx, maxq, s, r, z);
+            bad = !cache_grid<T>(mn, mx, maxq, s, r, z, edge);
+            edge = __any_sync(0xffffffffu, edge || bad);
             if (bad) {
                 s = __uint_as_float(0x7fffffffu);
                 r = 0.f;
@@ -215,38 +248,41 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
             p.scales[m] = s;
             if (FMT != GPTQ_CACHE_E4M3) p.zeros[m] = (uint8_t)z;
         }
-        const long long at = row * a.dim + (long long)g * a.group;  // element of the first code
+        unsigned char *code = p.codes + ((row * a.dim + (long long)g * a.group) >> (FMT == GPTQ_CACHE_INT4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int v = l + i * w;
-            if (v >= nvec) continue;
+            if (!a.full && v >= nvec) continue;
             float f[8];
             widen8(raw[i], f);
             if (FMT == GPTQ_CACHE_E4M3) {
                 if (bad) amax_finite8(f);
-                *reinterpret_cast<uint2 *>(p.codes + at + 8 * v) = e4m3_codes8(f, r);
+                *reinterpret_cast<uint2 *>(code + 8 * v) = e4m3_codes8(f, r);
             } else {
+                // x r + z rounded once, to a whole number in the low bits
                 constexpr float maxq = FMT == GPTQ_CACHE_INT4 ? 15.f : 255.f;
                 uint32_t c[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // x r + z rounded once, to a whole number; a group that is not finite has
-                    // r = 0 and gets code 0
-                    const float y = bad ? CACHE_MAGIC : fmaf(f[e], r, CACHE_MAGIC + z);
-                    c[e] = __float_as_uint(fminf(fmaxf(y, CACHE_MAGIC), CACHE_MAGIC + maxq));
+                for (int e = 0; e < 8; ++e) c[e] = __float_as_uint(fmaf(f[e], r, CACHE_MAGIC + z));
+                if (edge) {
+                    // a group that is not finite (r = 0, and NaN here at most) gets code 0
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        c[e] = bad ? 0u : __float_as_uint(fminf(fmaxf(__uint_as_float(c[e]), CACHE_MAGIC),
+                                                                CACHE_MAGIC + maxq));
                 }
                 if (FMT == GPTQ_CACHE_INT8) {
                     const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040),
                                                     __byte_perm(c[2], c[3], 0x0040), 0x5410);
                     const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040),
                                                     __byte_perm(c[6], c[7], 0x0040), 0x5410);
-                    *reinterpret_cast<uint2 *>(p.codes + at + 8 * v) = make_uint2(lo, hi);
+                    *reinterpret_cast<uint2 *>(code + 8 * v) = make_uint2(lo, hi);
                 } else {
                     // the low byte of c0 + 16 c1 is both codes: the bits above them in c0 and c1
                     // (2^23's) lie beyond it
                     const uint32_t lo = __byte_perm(c[0] + 16 * c[1], c[2] + 16 * c[3], 0x0040);
                     const uint32_t hi = __byte_perm(c[4] + 16 * c[5], c[6] + 16 * c[7], 0x0040);
-                    *reinterpret_cast<uint32_t *>(p.codes + (at >> 1) + 4 * v) = __byte_perm(lo, hi, 0x5410);
+                    *reinterpret_cast<uint32_t *>(code + 4 * v) = __byte_perm(lo, hi, 0x5410);
                 }
             }
         }
@@ -256,8 +292,6 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const __grid
 // ---------------------------------------------------------------------------------------
 // read
 // ---------------------------------------------------------------------------------------
-constexpr int CACHE_READ_UNROLL = 4;
-
 __device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
                  "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
@@ -292,81 +326,62 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float z, float *f) {
 // One unit is 8 U values; per_token.d units per token over the planes, per_plane.d per plane,
 // per_head.d per head, and per_group.d of them share a scale. U = 2 where heads and groups are
 // multiples of 16: what a unit's place costs is then shared by 16 values, and its 16-bit output
-// is one 32-byte store.
+// is one 32-byte store. A thread does one unit after another: several at once took more registers
+// than they saved waiting (131072 tokens of 8 x 128 at 8 bits: four at once 172 us, one 127 us).
 template <typename T, int FMT, int U>
-__global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const __grid_constant__ CacheArgs a) {
-    __shared__ long long slot[CACHE_MAX_TB];
+__global__ void __launch_bounds__(CACHE_THREADS, 8) cache_read_kernel(const __grid_constant__ CacheArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
     const int t0 = blockIdx.x * a.tb;
     const int nt = min(a.tb, a.tokens - t0);
-    if ((int)threadIdx.x < nt) {
-        long long s = a.slots[t0 + threadIdx.x];
-        if (s >= a.n_slots) {
-            report(GPTQ_ERR_ARG, t0 + (int)threadIdx.x);
-            s = -1;
-        }
-        slot[threadIdx.x] = s;
-    }
-    __syncthreads();
     const uint32_t units = (uint32_t)nt * a.per_token.d;
     const int row = a.heads * a.dim, meta = a.heads * (a.dim / a.group);
-    for (uint32_t u0 = threadIdx.x; u0 < units; u0 += CACHE_THREADS * CACHE_READ_UNROLL) {
-        uint2 c[CACHE_READ_UNROLL][U];
-        float s[CACHE_READ_UNROLL], z[CACHE_READ_UNROLL];
-        T *y[CACHE_READ_UNROLL];
-        int vec[CACHE_READ_UNROLL];
-#pragma unroll
-        for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
-            const uint32_t u = u0 + i * CACHE_THREADS;
-            y[i] = nullptr;
-            if (u >= units) continue;
-            const uint32_t j = a.per_token.div(u), rem = u - j * a.per_token.d;
-            const long long sl = slot[j];
-            if (sl < 0) continue;
-            const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d;
-            const CachePlane &p = a.p[pl];
-            const uint32_t h = a.per_head.div(v);
-            const long long at = sl * row + 8LL * U * v;
-            if (FMT == GPTQ_CACHE_INT4) {
-                if (U == 2) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(p.codes + (at >> 1));
-                    c[i][0].x = q.x;
-                    c[i][U - 1].x = q.y;
-                } else {
-                    c[i][0].x = *reinterpret_cast<const uint32_t *>(p.codes + (at >> 1));
-                }
-            } else if (U == 2 && a.vec) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(p.codes + at);
-                c[i][0] = make_uint2(q.x, q.y);
-                c[i][U - 1] = make_uint2(q.z, q.w);
-            } else {
-#pragma unroll
-                for (int k = 0; k < U; ++k) c[i][k] = *reinterpret_cast<const uint2 *>(p.codes + at + 8 * k);
-            }
-            const long long m = sl * meta + a.per_group.div(v);
-            s[i] = p.scales[m];
-            z[i] = FMT != GPTQ_CACHE_E4M3 ? (float)p.zeros[m] : 0.f;
-            y[i] = static_cast<T *>(p.y) + (long long)(t0 + (int)j) * p.ts + (long long)h * p.hs +
-                   8 * U * (v - h * a.per_head.d);
-            vec[i] = p.vec;
+    for (uint32_t u = threadIdx.x; u < units; u += CACHE_THREADS) {
+        const uint32_t j = a.per_token.div(u), rem = u - j * a.per_token.d;
+        const long long sl = a.slots[t0 + (int)j];
+        if (sl < 0) continue;
+        if (sl >= a.n_slots) {
+            if (rem == 0) report(GPTQ_ERR_ARG, t0 + (int)j);
+            continue;
         }
-#pragma unroll
-        for (int i = 0; i < CACHE_READ_UNROLL; ++i) {
-            if (!y[i]) continue;
-            float f[8 * U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) decode8<FMT>(c[i][k], s[i], z[i], f + 8 * k);
-            if (U == 2 && sizeof(T) == 2 && vec[i] == 2) {
-                uint4 o[2];
-                T *e = reinterpret_cast<T *>(o);
-#pragma unroll
-                for (int k = 0; k < 8 * U; ++k) e[k & 15] = narrow<T>(f[k]);
-                store32(y[i], o[0], o[1]);
+        const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d;
+        const CachePlane &p = a.p[pl];
+        const long long at = sl * row + 8LL * U * v;
+        uint2 c[U];
+        if (FMT == GPTQ_CACHE_INT4) {
+            if (U == 2) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(p.codes + (at >> 1));
+                c[0].x = q.x;
+                c[U - 1].x = q.y;
             } else {
-#pragma unroll
-                for (int k = 0; k < U; ++k) store8(y[i] + 8 * k, vec[i] != 0, f + 8 * k);
+                c[0].x = *reinterpret_cast<const uint32_t *>(p.codes + (at >> 1));
             }
+        } else if (U == 2 && a.vec) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p.codes + at);
+            c[0] = make_uint2(q.x, q.y);
+            c[U - 1] = make_uint2(q.z, q.w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k) c[k] = *reinterpret_cast<const uint2 *>(p.codes + at + 8 * k);
+        }
+        const long long m = sl * meta + a.per_group.div(v);
+        const float s = p.scales[m];
+        const float z = FMT != GPTQ_CACHE_E4M3 ? (float)p.zeros[m] : 0.f;
+        const uint32_t h = a.per_head.div(v);
+        T *y = static_cast<T *>(p.y) + (long long)(t0 + (int)j) * p.ts + (long long)h * p.hs +
+               8 * U * (v - h * a.per_head.d);
+        float f[8 * U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) decode8<FMT>(c[k], s, z, f + 8 * k);
+        if (U == 2 && sizeof(T) == 2 && p.vec == 2) {
+            uint4 o[2];
+            T *e = reinterpret_cast<T *>(o);
+#pragma unroll
+            for (int k = 0; k < 8 * U; ++k) e[k & 15] = narrow<T>(f[k]);
+            store32(y, o[0], o[1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k) store8(y + 8 * k, p.vec != 0, f + 8 * k);
         }
     }
 }
@@ -385,8 +400,10 @@ inline int cache_tokens_per_cta(int tokens, long long per_token) {
 template <typename T, int FMT>
 inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
     // four vectors of eight a lane: what a group costs once (its grid) is shared by 32 values
+    const int nvec = a.group / 8;
     a.w = 1;
-    while (4 * a.w < a.group / 8) a.w *= 2;
+    while (4 * a.w < nvec) a.w *= 2;
+    a.full = nvec == 4 * a.w && a.p[0].vec && (!a.p[1].x || a.p[1].vec);
     a.tb = cache_tokens_per_cta(a.tokens, (long long)a.per_token.d * a.w);
     const dim3 grid((a.tokens + a.tb - 1) / a.tb);
     return launch_kernel(cache_write_kernel<T, FMT>, grid, dim3(CACHE_THREADS), 0, s, true, a);
@@ -442,7 +459,7 @@ inline int cache_read(CacheArgs &a, int y_dtype, int format, cudaStream_t s) {
     a.per_plane = fast_div((uint32_t)a.heads * (a.dim / (8 * unit)));
     a.per_token = fast_div((uint32_t)planes * a.heads * (a.dim / (8 * unit)));
     a.per_group = fast_div(a.group / (8 * unit));
-    a.tb = cache_tokens_per_cta(a.tokens, (a.per_token.d + CACHE_READ_UNROLL - 1) / CACHE_READ_UNROLL);
+    a.tb = cache_tokens_per_cta(a.tokens, a.per_token.d);
     a.claims = nullptr;
     a.w = 1;
     // 16 codes at once

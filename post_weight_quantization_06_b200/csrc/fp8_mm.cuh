@@ -664,7 +664,7 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 // memory, four blocks at a time and a group ahead.
 //
 // With two accumulators (all of TMEM) what bounds a block is the way from its last MMA to the
-// release of its accumulator, about PAIR_CYCLES cycles, then the 1000 W power limit. One CTA per
+// release of its accumulator, about 900 cycles, then the 1000 W power limit. One CTA per
 // 128 x 256 tile has the shorter way (its commits and arrivals stay on the SM) but moves half as
 // much again; on random data it was 6 % slower. Accumulators of 128 columns, four of them, were
 // slower still: every wait and arrival doubles.

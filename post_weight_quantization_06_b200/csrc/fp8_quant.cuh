@@ -12,7 +12,7 @@ namespace gptq {
 namespace serve {
 
 struct Fp8QuantArgs {
-    const void *X;
+    const void *X, *X_end;   // X_end: behind the last value
     long long rows, cols, ldx, ldc;
     unsigned char *codes;
     float *scales;
@@ -32,44 +32,47 @@ __device__ __forceinline__ void store_codes8(unsigned char *p, bool vec, int hav
 }
 
 constexpr int FQ_THREADS = 256;
+constexpr int FQ_LANES = 4;
 
-// block_rows 1: four lanes per block, 32 values each (16-byte pieces l, l + 4, ... of the block's
+// block_rows 1: L lanes per block, 128 / L values each (pieces of eight l, l + L, ... of the block's
 // sixteen). The scale, its reciprocal and the block's place cost some 70 instructions, which at
-// 8 values a lane was more than all the rest: 16384 x 6144 bf16 in 88 us, with 32 in FQ_US us.
-template <typename T>
+// 8 values a lane was more than all the rest: 16384 x 6144 bf16 in 88 us, with 32 in 57 us.
+template <typename T, int L>
 __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_rows_kernel(Fp8QuantArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
-    const int l = threadIdx.x & 3;
-    const long long u = ((long long)blockIdx.x * FQ_THREADS + threadIdx.x) >> 2;
+    constexpr int V = 16 / L;
+    const int l = threadIdx.x & (L - 1);
+    const long long u = ((long long)blockIdx.x * FQ_THREADS + threadIdx.x) / L;
     const bool live = u < a.units;
     const uint32_t row = live ? (uint32_t)u / a.kb : 0, b = live ? (uint32_t)u - row * a.kb : 0;
     const long long left = live ? a.cols - (long long)b * 128 : 0;   // columns of the block, at most
     const T *x = static_cast<const T *>(a.X) + (long long)row * a.ldx + (long long)b * 128;
-    Raw8<T> raw[4];
+    Raw8<T> raw[V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = 8 * (l + 4 * i);
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (l + L * i);
         const int have = (int)max(0LL, min(8LL, left - c));
-        load8(have ? x + c : x, a.vec_in && have == 8, have, raw[i]);
+        if (a.vec_in || have < 8 || !load8_shifted(x + c, a.X, a.X_end, raw[i]))
+            load8(have ? x + c : x, a.vec_in && have == 8, have, raw[i]);
     }
     Amax<T> am;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) am.add(raw[i]);
+    for (int i = 0; i < V; ++i) am.add(raw[i]);
     float m = am.value();
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+    for (int o = L >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool bad = !finitef(m);
     if (__any_sync(0xffffffffu, bad)) {
         m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             float v[8];
             widen8(raw[i], v);
             m = fmaxf(m, amax_finite8(v));
         }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+        for (int o = L >> 1; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (bad && l == 0) report(GPTQ_ERR_NONFINITE, row);
     }
     if (!live) return;
@@ -77,8 +80,8 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_rows_kernel(Fp8QuantA
     if (l == 0) a.scales[(long long)row * a.kb + b] = s;
     unsigned char *y = a.codes + (long long)row * a.ldc + (long long)b * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = 8 * (l + 4 * i);
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (l + L * i);
         const int have = (int)max(0LL, min(8LL, left - c));
         if (!have) continue;
         float v[8];
@@ -89,26 +92,31 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_rows_kernel(Fp8QuantA
     }
 }
 
-// block_rows 128: a CTA per block, 64 values per thread (rows t / 16 + 16 i, columns 8 (t % 16)).
-template <typename T>
-__global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8QuantArgs a) {
+// block_rows 128: a CTA of N threads per block, 16384 / N values per thread (columns 8 (t % 16)). A
+// CTA loads, then computes: several per SM overlap. Four of 256 threads for 16-bit types, 8192 x
+// 8192 bf16 in 43 us (two of 512: 53 us); two of 512 for fp32, 5000 x 3001 in 24 us (two of 256: 32).
+template <typename T, int N>
+__global__ void __launch_bounds__(N, N == 256 ? 4 : 2) fp8_quantize_tiles_kernel(Fp8QuantArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
-    __shared__ float wmax[2][FQ_THREADS / 32];
+    __shared__ float wmax[2][N / 32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t br = blockIdx.x / a.kb, b = blockIdx.x - br * a.kb;
     const long long c = (long long)b * 128 + 8 * (t & 15);
     const int have = (int)max(0LL, min(8LL, a.cols - c));
-    Raw8<T> raw[8];
+    constexpr int V = 2048 / N, R = N / 16;   // vectors of a thread, rows between them
+    Raw8<T> raw[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long r = (long long)br * 128 + (t >> 4) + 16 * i;
+    for (int i = 0; i < V; ++i) {
+        const long long r = (long long)br * 128 + (t >> 4) + R * i;
         const int n = r < a.rows ? have : 0;
-        load8(static_cast<const T *>(a.X) + (n ? r * a.ldx + c : 0), a.vec_in && n == 8, n, raw[i]);
+        const T *x = static_cast<const T *>(a.X) + (n ? r * a.ldx + c : 0);
+        if (a.vec_in || n < 8 || !load8_shifted(x, a.X, a.X_end, raw[i]))
+            load8(x, a.vec_in && n == 8, n, raw[i]);
     }
     Amax<T> am;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am.add(raw[i]);
+    for (int i = 0; i < V; ++i) am.add(raw[i]);
     float m = am.value();
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -116,31 +124,31 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8Quant
     __syncthreads();
     m = 0.f;
 #pragma unroll
-    for (int w = 0; w < FQ_THREADS / 32; ++w) m = max_nan(m, wmax[0][w]);
+    for (int w = 0; w < N / 32; ++w) m = max_nan(m, wmax[0][w]);
     const bool bad = !finitef(m);   // the same in every thread
     if (bad) {
         m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
             float v[8];
             widen8(raw[i], v);
             Amax<T> one;
             one.add(raw[i]);
             if (!finitef(one.value()))
-                report(GPTQ_ERR_NONFINITE, (long long)br * 128 + (t >> 4) + 16 * i);
+                report(GPTQ_ERR_NONFINITE, (long long)br * 128 + (t >> 4) + R * i);
             m = fmaxf(m, amax_finite8(v));
         }
         m = warp_max(m);
         if (lane == 0) wmax[1][warp] = m;
         __syncthreads();
         m = 0.f;
-        for (int w = 0; w < FQ_THREADS / 32; ++w) m = fmaxf(m, wmax[1][w]);
+        for (int w = 0; w < N / 32; ++w) m = fmaxf(m, wmax[1][w]);
     }
     const float s = e4m3_scale(m), r = __frcp_rn(s);
     if (t == 0) a.scales[blockIdx.x] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long row = (long long)br * 128 + (t >> 4) + 16 * i;
+    for (int i = 0; i < V; ++i) {
+        const long long row = (long long)br * 128 + (t >> 4) + R * i;
         if (row >= a.rows || have == 0) continue;
         float v[8];
         widen8(raw[i], v);
@@ -152,18 +160,19 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_tiles_kernel(Fp8Quant
 template <typename T>
 inline int fp8_quantize_launch(const Fp8QuantArgs &a, int block_rows, cudaStream_t s) {
     if (block_rows == 1) {
-        const long long per = FQ_THREADS / 4;
-        return launch_kernel(fp8_quantize_rows_kernel<T>, dim3((unsigned)((a.units + per - 1) / per)),
+        const long long per = FQ_THREADS / FQ_LANES;
+        return launch_kernel(fp8_quantize_rows_kernel<T, FQ_LANES>, dim3((unsigned)((a.units + per - 1) / per)),
                              dim3(FQ_THREADS), 0, s, true, a);
     }
-    return launch_kernel(fp8_quantize_tiles_kernel<T>, dim3((unsigned)a.units), dim3(FQ_THREADS), 0,
-                         s, true, a);
+    constexpr int N = sizeof(T) == 2 ? 256 : 512;
+    return launch_kernel(fp8_quantize_tiles_kernel<T, N>, dim3((unsigned)a.units), dim3(N), 0, s, true, a);
 }
 
 inline int fp8_quantize(const void *X, int x_dtype, long long rows, long long cols, long long ldx,
                         int block_rows, void *codes, long long ldc, float *scales, cudaStream_t s) {
     Fp8QuantArgs a;
     a.X = X;
+    a.X_end = static_cast<const char *>(X) + ((rows - 1) * ldx + cols) * serve_dtype_bytes(x_dtype);
     a.rows = rows;
     a.cols = cols;
     a.ldx = ldx;

@@ -44,6 +44,29 @@ __device__ __forceinline__ void load8(const T *p, bool vec, int have, Raw8<T> &r
         for (int i = 0; i < 8; ++i) e[i] = i < have ? p[i] : narrow<T>(0.f);
     }
 }
+// All eight from an address of any alignment of T: the aligned 16-byte words around them, shifted
+// into place. False, with nothing read, where a word would reach outside [lo, hi).
+template <typename T>
+__device__ __forceinline__ bool load8_shifted(const T *p, const void *lo, const void *hi, Raw8<T> &r) {
+    constexpr int N = 4 * Raw8<T>::WORDS;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char *at = reinterpret_cast<const char *>(p) - off;
+    if (at < static_cast<const char *>(lo) || at + 4 * N + 16 > static_cast<const char *>(hi)) return false;
+    uint32_t w[N + 4];
+#pragma unroll
+    for (int i = 0; i < N + 4; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(at + 4 * i);
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+    uint32_t *o = reinterpret_cast<uint32_t *>(r.w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = sizeof(T) == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], 8 * (off & 2));
+    return true;
+}
 template <typename T>
 __device__ __forceinline__ void widen8(const Raw8<T> &r, float *v) {
     const T *e = reinterpret_cast<const T *>(r.w);
