@@ -122,39 +122,50 @@ def fp8_quantize(X: torch.Tensor, *, block_rows: int = 1):
     rows, cols = X.shape
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
+    dtype, ldx, stream = _code(X), _pitch(X, "X"), _stream_of(None, X.get_device())
+    dev = X.device
     pitch = (cols + 15) & -16
-    codes = X.new_empty((rows, pitch), dtype=_E4M3)
-    if pitch != cols:
-        codes = codes[:, :cols]
-    scales = X.new_empty((-(-rows // block_rows), (cols + 127) >> 7), dtype=torch.float32)
-    gptq_fp8_quantize(X, block_rows, codes, scales)
+    kb = (cols + 127) >> 7
+    codes = torch.empty_strided((rows, cols), (pitch, 1), dtype=_E4M3, device=dev)
+    scales = torch.empty_strided((-(-rows // block_rows), kb), (kb, 1), dtype=torch.float32, device=dev)
+    st = _fp8_quantize(X.data_ptr(), dtype, rows, cols, ldx, block_rows, codes.data_ptr(), pitch,
+                       scales.data_ptr(), stream)
+    if st:
+        raise GptqError(st, "gptq_fp8_quantize")
     return codes, scales
 
 
-def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
-                    Y: torch.Tensor, stream=None):
-    """Y (m x n, bf16 / fp16 / fp32) = A B^T for e4m3 codes A (m x k, scales m x ceil(k / 128))
-    and B (n x k, scales ceil(n / 128) x ceil(k / 128))."""
+def _matmul_args(A, sA, B, sB):
+    """Checks the operands. Returns (device, m, n, k, their addresses and pitches as the library
+    takes them)."""
     m, k = A.shape
     n, kn = B.shape
     kb = (k + 127) >> 7
-    _typed(A, _E4M3, "A")
-    _typed(B, _E4M3, "B")
-    _typed(sA, torch.float32, "sA")
-    _typed(sB, torch.float32, "sB")
+    if A.dtype is not _E4M3 or B.dtype is not _E4M3:
+        raise TypeError(f"A and B must be {_E4M3}")
+    if sA.dtype is not torch.float32 or sB.dtype is not torch.float32:
+        raise TypeError("sA and sB must be float32")
     if kn != k:
         raise ValueError("A and B must have the same number of columns")
     if sA.shape != (m, kb) or not sA.is_contiguous():
         raise ValueError("sA must be contiguous, m x ceil(k / 128)")
     if sB.shape != ((n + 127) >> 7, kb) or not sB.is_contiguous():
         raise ValueError("sB must be contiguous, ceil(n / 128) x ceil(k / 128)")
+    dev = A.get_device()
+    _same_device(dev, sA, B, sB)
+    return dev, m, n, k, (A.data_ptr(), _pitch(A, "A"), sA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
+                          sB.data_ptr())
+
+
+def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
+                    Y: torch.Tensor, stream=None):
+    """Y (m x n, bf16 / fp16 / fp32) = A B^T for e4m3 codes A (m x k, scales m x ceil(k / 128))
+    and B (n x k, scales ceil(n / 128) x ceil(k / 128))."""
+    dev, m, n, k, ops = _matmul_args(A, sA, B, sB)
     if Y.shape != (m, n):
         raise ValueError("Y must be m x n")
-    dev = A.get_device()
-    _same_device(dev, sA, B, sB, Y)
-    st = _fp8_matmul(A.data_ptr(), _pitch(A, "A"), sA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
-                     sB.data_ptr(), m, n, k, Y.data_ptr(), _code(Y), _pitch(Y, "Y"),
-                     _stream_of(stream, dev))
+    _same_device(dev, Y)
+    st = _fp8_matmul(*ops, m, n, k, Y.data_ptr(), _code(Y), _pitch(Y, "Y"), _stream_of(stream, dev))
     if st:
         raise GptqError(st, "gptq_fp8_matmul")
 
@@ -162,8 +173,15 @@ def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torc
 def fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, *,
                out_dtype=torch.bfloat16) -> torch.Tensor:
     """``gptq_fp8_matmul`` into a fresh m x n tensor of ``out_dtype``."""
-    Y = sA.new_empty((A.shape[0], B.shape[0]), dtype=out_dtype)
-    gptq_fp8_matmul(A, sA, B, sB, Y)
+    code = _DTYPES.get(out_dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    dev, m, n, k, ops = _matmul_args(A, sA, B, sB)
+    stream = _stream_of(None, dev)
+    Y = torch.empty_strided((m, n), (n, 1), dtype=out_dtype, device=A.device)
+    st = _fp8_matmul(*ops, m, n, k, Y.data_ptr(), code, n, stream)
+    if st:
+        raise GptqError(st, "gptq_fp8_matmul")
     return Y
 
 
@@ -171,22 +189,23 @@ def _row_bytes(fmt: int, head_dim: int) -> int:
     return head_dim // 2 if fmt == GPTQ_CACHE_INT4 else head_dim
 
 
-def _cache_plane(shape, fmt, groups, codes, scales, zeros):
-    """Addresses of the codes, scales and zero-points of K or V, checked against the cache."""
-    n, heads, dim = shape
+def _cache_plane(shape, meta, grid, dev, codes, scales, zeros):
+    """Addresses of the codes, scales and zero-points of K or V, checked against the cache: `shape`
+    of the codes and `meta` of the others."""
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
         raise TypeError("codes must be uint8 and scales float32")
-    if codes.shape != (n, heads, dim >> 1 if fmt == GPTQ_CACHE_INT4 else dim) \
-            or not codes.is_contiguous():
+    if codes.shape != shape or not codes.is_contiguous():
         raise ValueError("codes must be contiguous, n_slots x heads x bytes of a head")
-    if scales.shape != (n, heads, groups) or not scales.is_contiguous():
+    if scales.shape != meta or not scales.is_contiguous():
         raise ValueError("scales must be contiguous, n_slots x heads x groups")
-    if fmt == GPTQ_CACHE_E4M3:
+    if not grid:
+        _same_device(dev, codes, scales)
         return codes.data_ptr(), scales.data_ptr(), None
     if zeros.dtype is not torch.uint8:
         raise TypeError("zeros must be uint8")
-    if zeros.shape != scales.shape or not zeros.is_contiguous():
+    if zeros.shape != meta or not zeros.is_contiguous():
         raise ValueError("zeros must be contiguous and have the shape of scales")
+    _same_device(dev, codes, scales, zeros)
     return codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()
 
 
@@ -206,11 +225,13 @@ def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_
     n = codes_k.shape[0]
     if group_size < 0 or (group_size and d % group_size):
         raise ValueError("group_size must divide head_dim")
-    groups = d // group_size if group_size else 1
-    pk = _cache_plane((n, h, d), fmt, groups, codes_k, scales_k, zeros_k)
+    shape = (n, h, _row_bytes(fmt, d))
+    meta = (n, h, d // group_size if group_size else 1)
+    grid = fmt != GPTQ_CACHE_E4M3
     dev = K.get_device()
-    _same_device(dev, slots, codes_k, scales_k, zeros_k)
+    pk = _cache_plane(shape, meta, grid, dev, codes_k, scales_k, zeros_k)
     if V is None:
+        _same_device(dev, slots)
         return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (None, 0, 0), pk + _NO_PLANE
     if V.shape != K.shape:
         raise ValueError("V must have the shape of K")
@@ -218,8 +239,8 @@ def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_
     vt, vh, one = V.stride()
     if one != 1 and d > 1:
         raise ValueError("V: the values of a head must be contiguous")
-    pv = _cache_plane((n, h, d), fmt, groups, codes_v, scales_v, zeros_v)
-    _same_device(dev, V, codes_v, scales_v, zeros_v)
+    pv = _cache_plane(shape, meta, grid, dev, codes_v, scales_v, zeros_v)
+    _same_device(dev, slots, V)
     return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (V.data_ptr(), vt, vh), pk + pv
 
 
