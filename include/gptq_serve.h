@@ -16,6 +16,8 @@
  * workspace, allocates, or keeps anything between calls; all of them can be captured into a CUDA
  * graph, and run at once on several streams as long as they do not write the same memory.
  *
+ * Arrays start on a multiple of their element's size (more where it is said); others are refused.
+ *
  * e4m3: 1 sign, 4 exponent and 3 mantissa bits, largest value 448, no infinity, one NaN.
  */
 #ifndef GPTQ_SERVE_H

@@ -1,7 +1,8 @@
 // The quantized cache of keys and values (gptq_cache_write, gptq_cache_read).
 //
 // Write: a unit is one group of one head of one token of K or V. A power of two of lanes holds
-// it, up to 32 values each, between its range and its codes: one pass over the values. Read: a unit is eight values.
+// it, up to 32 values each, between its range and its codes: one pass over the values. Read: a unit
+// is 8 or 16 values.
 //   int:  s = max((mx - mn) / maxq, 2^-126), z = rint(-mn maxq / (mx - mn)),
 //         c = clamp(rint(x / s + z)), value s (c - z)
 //   e4m3: s = max(max |x| / 448, 2^-126), c = e4m3(x / s), value s c
@@ -176,7 +177,8 @@ struct WriteUnit {
 };
 
 template <typename T, int FMT>
-__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? 6 : 4) cache_write_kernel(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? 6 : 4)
+cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     __shared__ int beaten[CACHE_MAX_TB];
     pdl_launch_next();

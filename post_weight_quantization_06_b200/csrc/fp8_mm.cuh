@@ -893,9 +893,10 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 #pragma unroll
             for (int c = 0; c < 128 / C; ++c) {
                 if (n0 + C * c >= a.n || m0 >= a.m) continue;   // the same in the whole warp
-                // the slices take turns: the last store but one, from this one, has read it
+                // the slices take turns: the last TMA store but one, from this one, has read it
                 unsigned char *slice = slices + (turn & 1) * PAIR_SLICE;
-                ++turn;
+                // TMA stores whole 16-byte pieces, the last of a row too: past the columns
+                const bool tma = a.vec16 && (n0 + C * c + C <= a.n || a.n % E == 0);
                 if (a.vec16 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
 #pragma unroll
@@ -906,10 +907,11 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                     *reinterpret_cast<uint4 *>(slice + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                         *reinterpret_cast<const uint4 *>(v);
                 }
-                if (a.vec16) {
+                if (tma) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mm_store_2d(&ymap, slice, n0 + C * c, m0);
+                    ++turn;
                 } else {
                     __syncwarp();
                     store_slice(static_cast<TY *>(a.Y) + (long long)m0 * a.ldy + n0 + C * c, a.ldy, slice,

@@ -801,6 +801,9 @@ GPTQ_API int gptq_quantize_layer_reduced(const void *W, int w_dtype, int64_t m, 
 // ---------------------------------------------------------------------------------------
 // gptq_serve.h
 // ---------------------------------------------------------------------------------------
+// Whether an address is no multiple of `a` (a power of two).
+static bool off(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
 static int gptq_fp8_quantize_body(const void *X, int x_dtype, int64_t rows, int64_t cols,
                                   int64_t ldx, int block_rows, void *codes, int64_t ldc,
                                   float *scales, gptq_stream_t stream) {
@@ -808,6 +811,7 @@ static int gptq_fp8_quantize_body(const void *X, int x_dtype, int64_t rows, int6
     if (rows < 0 || cols < 0 || cols > 0x7fffffffLL || rows > 0x7fffffffLL) return GPTQ_ERR_ARG;
     if (rows == 0 || cols == 0) return GPTQ_OK;
     if (!X || !codes || !scales || ldx < cols || ldc < cols) return GPTQ_ERR_ARG;
+    if (off(X, serve::serve_dtype_bytes(x_dtype)) || off(scales, 4)) return GPTQ_ERR_ARG;
     if (rows * ((cols + 127) / 128) > 0x7fffffffLL) return GPTQ_ERR_ARG;
     return serve::fp8_quantize(X, x_dtype, rows, cols, ldx, block_rows, codes, ldc, scales,
                                reinterpret_cast<cudaStream_t>(stream));
@@ -828,13 +832,14 @@ static int gptq_fp8_matmul_body(const void *A, int64_t lda, const float *sA, con
     if (!serve::serve_dtype_ok(y_dtype)) return GPTQ_ERR_ARG;
     if (m < 0 || n < 0 || k < 0 || m > most || n > most || k > most) return GPTQ_ERR_ARG;
     if (m == 0 || n == 0) return GPTQ_OK;
-    if (!Y || ldy < n) return GPTQ_ERR_ARG;
+    if (!Y || ldy < n || off(Y, serve::serve_dtype_bytes(y_dtype))) return GPTQ_ERR_ARG;
     if (k > 0) {
         // the pitch of a single row is of no account
         if (m == 1) lda = (k + 15) / 16 * 16;
         if (n == 1) ldb = (k + 15) / 16 * 16;
         if (!A || !B || !sA || !sB || lda < k || ldb < k || lda % 16 || ldb % 16) return GPTQ_ERR_ARG;
-        if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) & 15u) return GPTQ_ERR_ARG;
+        if (lda >> 40 || ldb >> 40) return GPTQ_ERR_ARG;   // what a tensor map can hold
+        if (off(A, 16) || off(B, 16) || off(sA, 4) || off(sB, 4)) return GPTQ_ERR_ARG;
     }
     return serve::fp8_matmul(A, lda, sA, B, ldb, sB, m, n, k, Y, y_dtype, ldy,
                              reinterpret_cast<cudaStream_t>(stream));
@@ -864,8 +869,8 @@ static int cache_check(serve::CacheArgs &a, const int64_t *slots, int64_t tokens
     const bool grid = format != GPTQ_CACHE_E4M3;
     if (!slots || !codes_k || !scales_k || (grid && !zeros_k)) return GPTQ_ERR_ARG;
     if (two && (!codes_v || !scales_v || (grid && !zeros_v))) return GPTQ_ERR_ARG;
-    if ((reinterpret_cast<uintptr_t>(codes_k) | (two ? reinterpret_cast<uintptr_t>(codes_v) : 0)) & 7u)
-        return GPTQ_ERR_ARG;
+    if (off(slots, 8) || off(codes_k, 8) || off(scales_k, 4)) return GPTQ_ERR_ARG;
+    if (two && (off(codes_v, 8) || off(scales_v, 4))) return GPTQ_ERR_ARG;
     a.slots = slots;
     a.n_slots = n_slots;
     a.tokens = (int)tokens;
@@ -912,6 +917,9 @@ static int gptq_cache_write_body(const void *K, int64_t k_token_stride, int64_t 
         return st;
     if (tokens == 0) return GPTQ_OK;
     if (!K || (tokens > GPTQ_CACHE_UNCLAIMED && !claims)) return GPTQ_ERR_ARG;
+    if (off(K, serve::serve_dtype_bytes(x_dtype)) || off(V, serve::serve_dtype_bytes(x_dtype)) ||
+        off(claims, 4))
+        return GPTQ_ERR_ARG;
     a.claims = claims;
     a.p[0].x = K;
     a.p[0].ts = k_token_stride;
@@ -952,6 +960,8 @@ static int gptq_cache_read_body(const int64_t *slots, int64_t tokens, int64_t n_
     if (tokens == 0) return GPTQ_OK;
     if (!K || !rows_apart(tokens, heads, head_dim, k_token_stride, k_head_stride)) return GPTQ_ERR_ARG;
     if (V && !rows_apart(tokens, heads, head_dim, v_token_stride, v_head_stride)) return GPTQ_ERR_ARG;
+    if (off(K, serve::serve_dtype_bytes(y_dtype)) || off(V, serve::serve_dtype_bytes(y_dtype)))
+        return GPTQ_ERR_ARG;
     a.p[0].y = K;
     a.p[0].ts = k_token_stride;
     a.p[0].hs = k_head_stride;

@@ -291,3 +291,76 @@ def test_matmul_rows_of_any_alignment_at_large_sizes(g, n, dtype):
     at = torch.cat([torch.arange(0, 40), torch.arange(1270, 1300), torch.arange(2960, 3000)]).to(DEV)
     judge(Y[at], A.view(torch.uint8)[at].view(F8), sA[at], B, sB, dtype)
     assert torch.isfinite(Y).all()
+
+
+@pytest.mark.parametrize("n,ldy,dtype", [(2630, 2640, "bf16"), (2631, 2632, "fp16"), (2601, 2604, "fp32"),
+                                         (2630, 2643, "bf16")])
+def test_matmul_into_a_pitched_output_at_large_sizes(g, n, ldy, dtype):
+    m, k = 2900, 260
+    A, sA, B, sB = operands(g, m, n, k, seed=3)
+    out = torch.full((m + 1, ldy), -7.0, device=DEV, dtype=DT[dtype])
+    g.gptq_fp8_matmul(A, sA, B, sB, out[:m, :n])
+    g.gptq_sync_status()
+    at = torch.cat([torch.arange(0, 20), torch.arange(2860, 2900)]).to(DEV)
+    judge(out[at, :n], A.view(torch.uint8)[at].view(F8), sA[at], B, sB, dtype)
+    assert torch.isfinite(out).all()
+    assert (out[m:] == -7).all() and (out[:, n:] == -7).all()
+
+
+def test_capture_that_forks_and_joins(g):
+    """The two operands are quantized on two captured streams and multiplied after the join."""
+    m, n, k = 100, 384, 512
+    X, W = values(m, k, "bf16", seed=1), values(n, k, "bf16", seed=2)
+    A, sA = g.fp8_quantize(X)
+    B, sB = g.fp8_quantize(W, block_rows=128)
+    Y = torch.zeros(m, n, device=DEV)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        g.gptq_fp8_quantize(X, 1, A, sA)
+        with torch.cuda.stream(side):
+            g.gptq_fp8_quantize(W, 128, B, sB)
+        main.wait_stream(side)
+        g.gptq_fp8_matmul(A, sA, B, sB, Y)
+        Y.mul_(2.0)
+    for seed in (5, 6):
+        X.copy_(values(m, k, "bf16", seed=seed))
+        W.copy_(values(n, k, "bf16", seed=seed + 10))
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = g.fp8_quantize(X), g.fp8_quantize(W, block_rows=128)
+        assert torch.equal(Y, 2 * g.fp8_matmul(*a, *b, out_dtype=torch.float32))
+    g.gptq_sync_status()
+
+
+FIRST = """
+import torch, post_weight_quantization_06_b200 as g
+x = torch.randn(40, 256, device="cuda"); w = torch.randn(300, 256, device="cuda")
+at = torch.arange(600, device="cuda") % 300
+kv = torch.randn(600, 2, 64, device="cuda", dtype=torch.bfloat16)
+c = g.kv_cache(300, 2, 64)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = g.fp8_matmul(*g.fp8_quantize(x), *g.fp8_quantize(w, block_rows=128))
+    g.cache_write(c, kv, kv, at)
+    k, v = g.cache_read(c, at)
+graph.replay()
+torch.cuda.synchronize()
+want = g.fp8_matmul(*g.fp8_quantize(x), *g.fp8_quantize(w, block_rows=128))
+g.cache_write(c, kv, kv, at)
+assert torch.equal(y, want) and torch.equal(k, g.cache_read(c, at)[0]) and torch.equal(k, v)
+g.gptq_sync_status()
+print("ok")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stderr[-2000:]

@@ -143,3 +143,28 @@ def test_binding_refuses_host_tensors_types_and_shapes():
             g.kv_cache(10, 2, 64, device="cpu", **kw)
     with pytest.raises(ValueError):
         g.kv_cache(10, 2, 60, device="cpu")
+
+
+R = ctypes.c_void_p(258)   # a multiple of 2 only
+
+
+@pytest.mark.parametrize("kw", [dict(X=Q), dict(X=R, dt=1), dict(scales=R)])
+def test_quantize_refuses_addresses_no_element_starts_at(kw):
+    refused("gptq_fp8_quantize", {**QUANT, **kw}.values())
+
+
+@pytest.mark.parametrize("kw", [dict(Y=Q), dict(Y=R, dt=1), dict(sA=R), dict(sB=Q),
+                                dict(lda=1 << 41), dict(ldb=1 << 40)])
+def test_matmul_refuses_addresses_and_pitches_out_of_range(kw):
+    refused("gptq_fp8_matmul", {**MM, **kw}.values())
+
+
+@pytest.mark.parametrize("kw", [dict(K=Q), dict(V=R, dt=1), dict(slots=R), dict(sk=R), dict(sv=Q),
+                                dict(claims=R)])
+def test_write_refuses_addresses_no_element_starts_at(kw):
+    refused("gptq_cache_write", {**WRITE, **kw}.values())
+
+
+@pytest.mark.parametrize("kw", [dict(K=R, dt=1), dict(V=Q), dict(slots=R), dict(sk=Q)])
+def test_read_refuses_addresses_no_element_starts_at(kw):
+    refused("gptq_cache_read", {**READ, **kw}.values())
