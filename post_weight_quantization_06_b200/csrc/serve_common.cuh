@@ -186,9 +186,10 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 // that to e4m3 rounds the exact product (a nearest product could itself land on a border
 // between two codes, which would then be decided by the even one).
 __device__ __forceinline__ float mul_sticky(float x, float r) {
-    const float p = __fmul_rz(x, r);
-    const float d = __fmaf_rn(x, r, -p);
-    return d != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+    uint32_t p = __float_as_uint(__fmul_rz(x, r));
+    const float d = __fmaf_rn(x, r, -__uint_as_float(p));
+    asm("{\n\t.reg .pred q;\n\tsetp.neu.f32 q, %1, 0f00000000;\n\t@q or.b32 %0, %0, 1;\n\t}" : "+r"(p) : "f"(d));
+    return __uint_as_float(p);
 }
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     uint16_t d;
