@@ -21,7 +21,7 @@ GPTQ_CACHE_UNCLAIMED = 512
 EXPORTED_SERVE = ("gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_cache_write", "gptq_cache_read")
 
 _DTYPES = {torch.bfloat16: GPTQ_BF16, torch.float32: GPTQ_F32, torch.float16: GPTQ_F16}
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _F32, _U8 = torch.float8_e4m3fn, torch.float32, torch.uint8
 
 
 def _bind():
@@ -57,21 +57,13 @@ def _stream_of(stream, dev: int) -> int:
     return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _same_device(dev: int, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"one of the tensors is on {t.device}: all must be on the "
-                             "current device")
+def _devices_differ():
+    raise ValueError("the tensors must all be on the current device")
 
 
 def _want(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
-
-
-def _typed(t: torch.Tensor, dtype, name: str):
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
 def _code(t: torch.Tensor) -> int:
@@ -99,16 +91,19 @@ def gptq_fp8_quantize(X: torch.Tensor, block_rows: int, codes: torch.Tensor, sca
     """codes (e4m3, as X), scales (fp32) = X (rows x cols, bf16 / fp16 / fp32, any row pitch) in
     8-bit floating point with one scale per block of ``block_rows`` (1 or 128) x 128."""
     rows, cols = X.shape
-    _typed(codes, _E4M3, "codes")
-    _typed(scales, torch.float32, "scales")
-    if codes.shape != X.shape:
+    if codes.dtype is not _E4M3:
+        raise TypeError(f"codes must be {_E4M3}, got {codes.dtype}")
+    if scales.dtype is not _F32:
+        raise TypeError(f"scales must be {_F32}, got {scales.dtype}")
+    if codes.shape != (rows, cols):
         raise ValueError("codes must have the shape of X")
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     if scales.shape != (-(-rows // block_rows), (cols + 127) >> 7) or not scales.is_contiguous():
         raise ValueError("scales must be contiguous, ceil(rows / block_rows) x ceil(cols / 128)")
     dev = X.get_device()
-    _same_device(dev, codes, scales)
+    if codes.get_device() != dev or scales.get_device() != dev:
+        _devices_differ()
     st = _fp8_quantize(X.data_ptr(), _code(X), rows, cols, _pitch(X, "X"), block_rows,
                        codes.data_ptr(), _pitch(codes, "codes"), scales.data_ptr(),
                        _stream_of(stream, dev))
@@ -127,7 +122,7 @@ def fp8_quantize(X: torch.Tensor, *, block_rows: int = 1):
     pitch = (cols + 15) & -16
     kb = (cols + 127) >> 7
     codes = torch.empty_strided((rows, cols), (pitch, 1), dtype=_E4M3, device=dev)
-    scales = torch.empty_strided((-(-rows // block_rows), kb), (kb, 1), dtype=torch.float32, device=dev)
+    scales = torch.empty_strided((-(-rows // block_rows), kb), (kb, 1), dtype=_F32, device=dev)
     st = _fp8_quantize(X.data_ptr(), dtype, rows, cols, ldx, block_rows, codes.data_ptr(), pitch,
                        scales.data_ptr(), stream)
     if st:
@@ -135,37 +130,41 @@ def fp8_quantize(X: torch.Tensor, *, block_rows: int = 1):
     return codes, scales
 
 
-def _matmul_args(A, sA, B, sB):
-    """Checks the operands. Returns (device, m, n, k, their addresses and pitches as the library
-    takes them)."""
-    m, k = A.shape
-    n, kn = B.shape
+def _bad_operands(A, sA, B, sB):
+    """Raises for the first thing that is wrong with the operands of a product."""
+    (m, k), (n, kn) = A.shape, B.shape
     kb = (k + 127) >> 7
     if A.dtype is not _E4M3 or B.dtype is not _E4M3:
         raise TypeError(f"A and B must be {_E4M3}")
-    if sA.dtype is not torch.float32 or sB.dtype is not torch.float32:
-        raise TypeError("sA and sB must be float32")
+    if sA.dtype is not _F32 or sB.dtype is not _F32:
+        raise TypeError(f"sA and sB must be {_F32}")
     if kn != k:
         raise ValueError("A and B must have the same number of columns")
     if sA.shape != (m, kb) or not sA.is_contiguous():
         raise ValueError("sA must be contiguous, m x ceil(k / 128)")
-    if sB.shape != ((n + 127) >> 7, kb) or not sB.is_contiguous():
-        raise ValueError("sB must be contiguous, ceil(n / 128) x ceil(k / 128)")
-    dev = A.get_device()
-    _same_device(dev, sA, B, sB)
-    return dev, m, n, k, (A.data_ptr(), _pitch(A, "A"), sA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
-                          sB.data_ptr())
+    raise ValueError("sB must be contiguous, ceil(n / 128) x ceil(k / 128)")
 
 
 def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
                     Y: torch.Tensor, stream=None):
     """Y (m x n, bf16 / fp16 / fp32) = A B^T for e4m3 codes A (m x k, scales m x ceil(k / 128))
     and B (n x k, scales ceil(n / 128) x ceil(k / 128))."""
-    dev, m, n, k, ops = _matmul_args(A, sA, B, sB)
+    m, k = A.shape
+    n, kn = B.shape
+    kb = (k + 127) >> 7
+    if (A.dtype is not _E4M3 or B.dtype is not _E4M3 or sA.dtype is not _F32 or sB.dtype is not _F32
+            or kn != k or sA.shape != (m, kb) or sB.shape != ((n + 127) >> 7, kb)
+            or not sA.is_contiguous() or not sB.is_contiguous()):
+        _bad_operands(A, sA, B, sB)
     if Y.shape != (m, n):
         raise ValueError("Y must be m x n")
-    _same_device(dev, Y)
-    st = _fp8_matmul(*ops, m, n, k, Y.data_ptr(), _code(Y), _pitch(Y, "Y"), _stream_of(stream, dev))
+    dev = A.get_device()
+    if (sA.get_device() != dev or B.get_device() != dev or sB.get_device() != dev
+            or Y.get_device() != dev):
+        _devices_differ()
+    st = _fp8_matmul(A.data_ptr(), _pitch(A, "A"), sA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
+                     sB.data_ptr(), m, n, k, Y.data_ptr(), _code(Y), _pitch(Y, "Y"),
+                     _stream_of(stream, dev))
     if st:
         raise GptqError(st, "gptq_fp8_matmul")
 
@@ -173,15 +172,11 @@ def gptq_fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torc
 def fp8_matmul(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, *,
                out_dtype=torch.bfloat16) -> torch.Tensor:
     """``gptq_fp8_matmul`` into a fresh m x n tensor of ``out_dtype``."""
-    code = _DTYPES.get(out_dtype)
-    if code is None:
+    if out_dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {out_dtype}")
-    dev, m, n, k, ops = _matmul_args(A, sA, B, sB)
-    stream = _stream_of(None, dev)
+    m, n = A.shape[0], B.shape[0]
     Y = torch.empty_strided((m, n), (n, 1), dtype=out_dtype, device=A.device)
-    st = _fp8_matmul(*ops, m, n, k, Y.data_ptr(), code, n, stream)
-    if st:
-        raise GptqError(st, "gptq_fp8_matmul")
+    gptq_fp8_matmul(A, sA, B, sB, Y)
     return Y
 
 
@@ -192,20 +187,22 @@ def _row_bytes(fmt: int, head_dim: int) -> int:
 def _cache_plane(shape, meta, grid, dev, codes, scales, zeros):
     """Addresses of the codes, scales and zero-points of K or V, checked against the cache: `shape`
     of the codes and `meta` of the others."""
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
+    if codes.dtype is not _U8 or scales.dtype is not _F32:
         raise TypeError("codes must be uint8 and scales float32")
     if codes.shape != shape or not codes.is_contiguous():
         raise ValueError("codes must be contiguous, n_slots x heads x bytes of a head")
     if scales.shape != meta or not scales.is_contiguous():
         raise ValueError("scales must be contiguous, n_slots x heads x groups")
+    if codes.get_device() != dev or scales.get_device() != dev:
+        _devices_differ()
     if not grid:
-        _same_device(dev, codes, scales)
         return codes.data_ptr(), scales.data_ptr(), None
-    if zeros.dtype is not torch.uint8:
+    if zeros.dtype is not _U8:
         raise TypeError("zeros must be uint8")
     if zeros.shape != meta or not zeros.is_contiguous():
         raise ValueError("zeros must be contiguous and have the shape of scales")
-    _same_device(dev, codes, scales, zeros)
+    if zeros.get_device() != dev:
+        _devices_differ()
     return codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()
 
 
@@ -216,7 +213,8 @@ def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_
     """Checks what both cache calls take. Returns (device, slots of the cache, (tokens, heads,
     head_dim), address and strides of K, of V, addresses of the cache's arrays)."""
     t, h, d = K.shape
-    _typed(slots, torch.int64, "slots")
+    if slots.dtype is not torch.int64:
+        raise TypeError(f"slots must be {torch.int64}, got {slots.dtype}")
     if slots.shape != (t,) or not slots.is_contiguous():
         raise ValueError("slots must be one number per token")
     kt, kh, one = K.stride()
@@ -225,22 +223,25 @@ def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_
     n = codes_k.shape[0]
     if group_size < 0 or (group_size and d % group_size):
         raise ValueError("group_size must divide head_dim")
-    shape = (n, h, _row_bytes(fmt, d))
+    shape = (n, h, d >> 1 if fmt == GPTQ_CACHE_INT4 else d)
     meta = (n, h, d // group_size if group_size else 1)
     grid = fmt != GPTQ_CACHE_E4M3
     dev = K.get_device()
+    if slots.get_device() != dev:
+        _devices_differ()
     pk = _cache_plane(shape, meta, grid, dev, codes_k, scales_k, zeros_k)
     if V is None:
-        _same_device(dev, slots)
         return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (None, 0, 0), pk + _NO_PLANE
-    if V.shape != K.shape:
+    if V.shape != (t, h, d):
         raise ValueError("V must have the shape of K")
-    _typed(V, K.dtype, "V")
+    if V.dtype is not K.dtype:
+        raise TypeError(f"V must be {K.dtype}, got {V.dtype}")
     vt, vh, one = V.stride()
     if one != 1 and d > 1:
         raise ValueError("V: the values of a head must be contiguous")
+    if V.get_device() != dev:
+        _devices_differ()
     pv = _cache_plane(shape, meta, grid, dev, codes_v, scales_v, zeros_v)
-    _same_device(dev, slots, V)
     return dev, n, (t, h, d), (K.data_ptr(), kt, kh), (V.data_ptr(), vt, vh), pk + pv
 
 
@@ -255,10 +256,12 @@ def gptq_cache_write(K: torch.Tensor, V: torch.Tensor | None, slots: torch.Tenso
                                             codes_v, scales_v, zeros_v)
     cp = None
     if claims is not None:
-        _typed(claims, torch.int32, "claims")
+        if claims.dtype is not torch.int32:
+            raise TypeError(f"claims must be {torch.int32}, got {claims.dtype}")
         if claims.shape != (n,) or not claims.is_contiguous():
             raise ValueError("claims must be one number per slot")
-        _same_device(dev, claims)
+        if claims.get_device() != dev:
+            _devices_differ()
         cp = claims.data_ptr()
     st = _cache_write(*k, *v, _code(K), *thd, slots.data_ptr(), n, fmt, group_size, *planes, cp,
                       _stream_of(stream, dev))
