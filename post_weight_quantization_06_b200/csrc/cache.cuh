@@ -313,11 +313,17 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float z, float *f) {
     } else {
         // a code in the low bits of 2^23 is 2^23 + code: the difference is exact
         const float bias = 8388608.f + z;
+        if (FMT == GPTQ_CACHE_INT4) {
+            // the even codes and the odd ones, a byte each
+            const uint32_t odd = (c.x >> 4) & 0x0f0f0f0fu;
+            c.x &= 0x0f0f0f0fu;
+            c.y = odd;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            uint32_t q;
-            if (FMT == GPTQ_CACHE_INT4) q = ((c.x >> (4 * e)) & 15u) | 0x4b000000u;
-            else q = __byte_perm(e < 4 ? c.x : c.y, 0x4b000000u, 0x7440u | (e & 3));
+            const bool second = FMT == GPTQ_CACHE_INT4 ? e & 1 : e > 3;
+            const uint32_t at = FMT == GPTQ_CACHE_INT4 ? e >> 1 : e & 3;
+            const uint32_t q = __byte_perm(second ? c.y : c.x, 0x4b000000u, 0x7440u | at);
             f[e] = (__uint_as_float(q) - bias) * s;
         }
     }
