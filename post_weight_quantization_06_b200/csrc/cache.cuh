@@ -1,7 +1,7 @@
 // The quantized cache of keys and values (gptq_cache_write, gptq_cache_read).
 //
 // Write: a unit is one group of one head of one token of K or V. A power of two of lanes holds
-// it, up to 32 values each, between its range and its codes: one pass over the values. Read: a unit
+// it, up to 48 values each, between its range and its codes: one pass over the values. Read: a unit
 // is 8 or 16 values.
 //   int:  s = max((mx - mn) / maxq, 2^-126), z = rint(-mn maxq / (mx - mn)),
 //         c = clamp(rint(x / s + z)), value s (c - z)
@@ -42,7 +42,7 @@ struct CacheArgs {
     FastDiv per_token, per_plane, per_head, per_group;  // units (see each kernel)
     int w;                          // lanes of a unit (write)
     int vec;                        // codes take 16-byte accesses (read)
-    int full;                       // every lane has four vectors, all aligned (write)
+    int full;                       // every lane has all its vectors, aligned (write)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -154,7 +154,7 @@ struct WriteUnit {
         h = a.per_head.div(hg);
         g = hg - h * a.per_head.d;
     }
-    template <typename T>
+    template <int V, typename T>
     __device__ __forceinline__ void load(const CacheArgs &a, int t0, int l, int nvec, Raw8<T> *raw) const {
         const CachePlane &p = a.p[pl];
         const T *x = static_cast<const T *>(p.x) + (long long)(t0 + (int)j) * p.ts +
@@ -162,11 +162,11 @@ struct WriteUnit {
         if (a.full) {   // units that do not exist read the first token's
             x += 8 * l;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load8(x + i * 8 * a.w, true, 8, raw[i]);
+            for (int i = 0; i < V; ++i) load8(x + i * 8 * a.w, true, 8, raw[i]);
             return;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             const int v = l + i * a.w;
             const bool on = live && v < nvec;
             load8(x + (on ? 8 * v : 0), on && p.vec, on ? 8 : 0, raw[i]);
@@ -174,8 +174,8 @@ struct WriteUnit {
     }
 };
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? 6 : 4)
+template <typename T, int FMT, int V>
+__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? (V == 4 ? 6 : 5) : (V == 4 ? 4 : 3))
 cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     __shared__ int beaten[CACHE_MAX_TB];
@@ -189,14 +189,14 @@ cache_write_kernel(const __grid_constant__ CacheArgs a) {
     const int nvec = a.group >> 3;
     // the first values are on their way while the slots are looked at
     WriteUnit at0;
-    Raw8<T> raw[4];
+    Raw8<T> raw[V];
     at0.place(a, threadIdx.x / w, units);
-    at0.load(a, t0, l, nvec, raw);
+    at0.load<V>(a, t0, l, nvec, raw);
     cache_resolve(a, t0, nt, slot, beaten);
     for (uint32_t u0 = 0; u0 < units; u0 += step) {
         if (u0) {
             at0.place(a, u0 + threadIdx.x / w, units);
-            at0.load(a, t0, l, nvec, raw);
+            at0.load<V>(a, t0, l, nvec, raw);
         }
         const uint32_t j = at0.j, h = at0.h, g = at0.g;
         const CachePlane &p = a.p[at0.pl];
@@ -206,14 +206,14 @@ cache_write_kernel(const __grid_constant__ CacheArgs a) {
         if (FMT == GPTQ_CACHE_E4M3) {
             Amax<T> am;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) am.add(raw[i]);
+            for (int i = 0; i < V; ++i) am.add(raw[i]);
             float m = am.value();
             for (int o = w >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
             bad = !finitef(m);
             if (__any_sync(0xffffffffu, bad)) {
                 m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < V; ++i) {
                     float v[8];
                     widen8(raw[i], v);
                     m = fmaxf(m, amax_finite8(v));
@@ -226,7 +226,7 @@ cache_write_kernel(const __grid_constant__ CacheArgs a) {
             constexpr float maxq = FMT == GPTQ_CACHE_INT4 ? 15.f : 255.f;
             MinMax<T> mm;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mm.add(raw[i]);
+            for (int i = 0; i < V; ++i) mm.add(raw[i]);
             float mn = mm.low(), mx = mm.high();
             for (int o = w >> 1; o; o >>= 1) {
                 mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -250,7 +250,7 @@ cache_write_kernel(const __grid_constant__ CacheArgs a) {
         }
         unsigned char *code = p.codes + ((row * a.dim + (long long)g * a.group) >> (FMT == GPTQ_CACHE_INT4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             const int v = l + i * w;
             if (!a.full && v >= nvec) continue;
             float f[8];
@@ -405,14 +405,20 @@ inline int cache_tokens_per_cta(int tokens, long long per_token) {
 
 template <typename T, int FMT>
 inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
-    // four vectors of eight a lane: what a group costs once (its grid) is shared by 32 values
+    // Four or six vectors of eight a lane: what a group costs once (its grid) is shared by up to 48
+    // values. Six in long calls where that leaves fewer of them empty (heads of 80, 96, 192: 32768
+    // tokens of 16 x 80 at 4 bits 73 us with four, 53 us with six; 64 tokens of 8 x 96 3.4 and 3.9 us).
     const int nvec = a.group / 8;
-    a.w = 1;
-    while (4 * a.w < nvec) a.w *= 2;
-    a.full = nvec == 4 * a.w && a.p[0].vec && (!a.p[1].x || a.p[1].vec);
+    int w4 = 1, w6 = 1;
+    while (4 * w4 < nvec) w4 *= 2;
+    while (6 * w6 < nvec) w6 *= 2;
+    const bool six = a.tokens > GPTQ_CACHE_UNCLAIMED && 6 * w6 < 4 * w4;
+    a.w = six ? w6 : w4;
+    a.full = nvec == (six ? 6 : 4) * a.w && a.p[0].vec && (!a.p[1].x || a.p[1].vec);
     a.tb = cache_tokens_per_cta(a.tokens, (long long)a.per_token.d * a.w);
     const dim3 grid((a.tokens + a.tb - 1) / a.tb);
-    return launch_kernel(cache_write_kernel<T, FMT>, grid, dim3(CACHE_THREADS), 0, s, true, a);
+    if (six) return launch_kernel(cache_write_kernel<T, FMT, 6>, grid, dim3(CACHE_THREADS), 0, s, true, a);
+    return launch_kernel(cache_write_kernel<T, FMT, 4>, grid, dim3(CACHE_THREADS), 0, s, true, a);
 }
 template <typename T>
 inline int cache_write_fmt(CacheArgs &a, int format, cudaStream_t s) {
