@@ -95,19 +95,21 @@ __global__ void __launch_bounds__(FQ_THREADS) fp8_quantize_rows_kernel(Fp8QuantA
     }
 }
 
-// block_rows 128: a CTA of N threads per block, 16384 / N values per thread (columns 8 (t % 16)). A
-// CTA loads, then computes: several per SM overlap. Four of 256 threads for 16-bit types, 8192 x
-// 8192 bf16 in 43 us (two of 512: 53 us); two of 512 for fp32, 5000 x 3001 in 24 us (two of 256: 32).
-template <typename T, int N>
-__global__ void __launch_bounds__(N, N == 256 ? 4 : 2) fp8_quantize_tiles_kernel(Fp8QuantArgs a) {
+// block_rows 128: a CTA per block, 32 values per thread (rows t / 16 + 32 i, columns 8 (t % 16)). A CTA
+// loads, then computes: several per SM overlap. Three of 512 threads for 16-bit types (8192 x 8192
+// bf16 in 45 us, 5000 x 3001 in 18 us; four of 256, whose unaligned loads spill, 43 and 20 us), two for fp32
+// (2047 x 6100 in 14 us, 8192 x 8192 in 57 us = 5.9 TB/s; one of 1024, 90 us).
+constexpr int FQ_TILE_THREADS = 512;
+template <typename T>
+__global__ void __launch_bounds__(FQ_TILE_THREADS, sizeof(T) == 2 ? 3 : 2) fp8_quantize_tiles_kernel(Fp8QuantArgs a) {
     pdl_launch_next();
     pdl_wait_prev();
-    __shared__ float wmax[2][N / 32];
+    __shared__ float wmax[2][FQ_TILE_THREADS / 32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t br = blockIdx.x / a.kb, b = blockIdx.x - br * a.kb;
     const long long c = (long long)b * 128 + 8 * (t & 15);
     const int have = (int)max(0LL, min(8LL, a.cols - c));
-    constexpr int V = 2048 / N, R = N / 16;   // vectors of a thread, rows between them
+    constexpr int V = 2048 / FQ_TILE_THREADS, R = FQ_TILE_THREADS / 16;   // vectors of a thread, rows between them
     Raw8<T> raw[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(N, N == 256 ? 4 : 2) fp8_quantize_tiles_kernel
     __syncthreads();
     m = 0.f;
 #pragma unroll
-    for (int w = 0; w < N / 32; ++w) m = max_nan(m, wmax[0][w]);
+    for (int w = 0; w < FQ_TILE_THREADS / 32; ++w) m = max_nan(m, wmax[0][w]);
     const bool bad = !finitef(m);   // the same in every thread
     if (bad) {
         m = 0.f;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(N, N == 256 ? 4 : 2) fp8_quantize_tiles_kernel
         if (lane == 0) wmax[1][warp] = m;
         __syncthreads();
         m = 0.f;
-        for (int w = 0; w < N / 32; ++w) m = fmaxf(m, wmax[1][w]);
+        for (int w = 0; w < FQ_TILE_THREADS / 32; ++w) m = fmaxf(m, wmax[1][w]);
     }
     const float s = e4m3_scale(m), r = __frcp_rn(s);
     if (t == 0) a.scales[blockIdx.x] = s;
@@ -167,8 +169,8 @@ inline int fp8_quantize_launch(const Fp8QuantArgs &a, int block_rows, cudaStream
         return launch_kernel(fp8_quantize_rows_kernel<T, FQ_LANES>, dim3((unsigned)((a.units + per - 1) / per)),
                              dim3(FQ_THREADS), 0, s, true, a);
     }
-    constexpr int N = sizeof(T) == 2 ? 256 : 512;
-    return launch_kernel(fp8_quantize_tiles_kernel<T, N>, dim3((unsigned)a.units), dim3(N), 0, s, true, a);
+    return launch_kernel(fp8_quantize_tiles_kernel<T>, dim3((unsigned)a.units), dim3(FQ_TILE_THREADS), 0,
+                         s, true, a);
 }
 
 inline int fp8_quantize(const void *X, int x_dtype, long long rows, long long cols, long long ldx,
