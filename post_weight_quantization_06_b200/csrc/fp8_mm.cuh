@@ -665,28 +665,32 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 // memory and leave rows 128 r .. of the tile in CTA r's TMEM. A block of K takes the tensor cores
 // 512 cycles; in that time a promotion thread reads 128 columns of its row from one of two
 // accumulators and adds them to 128 sums in registers (setmaxnreg: 232 for the promotion warps,
-// 40 for the others, together the 168 x 384 of the launch). Its row's scales come straight from
-// memory, four blocks at a time and a group ahead.
+// 40 for the others, together the 168 x 384 of the launch). A warp of its own brings the scales to
+// shared memory, four blocks at a time and up to sixteen ahead; loaded by the promotion threads
+// themselves, four blocks ahead, they cost 5 % with 48 blocks a tile and 15 % with three, where a
+// tile's first scales were waited for. Their ring takes the place of a fifth stage of A and B.
 //
 // With two accumulators (all of TMEM) what bounds a block is the way from its last MMA to the
-// release of its accumulator, about 900 cycles, then the 1000 W power limit. One CTA per
+// release of its accumulator, about 840 cycles, then the 1000 W power limit. One CTA per
 // 128 x 256 tile has the shorter way (its commits and arrivals stay on the SM) but moves half as
 // much again; on random data it was 6 % slower. Accumulators of 128 columns, four of them, were
-// slower still: every wait and arrival doubles. 16384 x 2048 x 6144 in 182 us (2260 TFLOP/s, tensor pipe
-// busy 57 % of the time), 217 us in a loop that heats the card to its limit.
+// slower still: every wait and arrival doubles. 16384 x 2048 x 6144 in 174 us (2370 TFLOP/s, tensor
+// pipe busy 62 % of the time), 204 us in a loop that heats the card to its limit.
 //
-// Warps: 0 TMA, 1 TMEM and (leader) MMA, 4-11 promotion (32 rows x 128 columns each). A tile's sums
-// are rounded into shared memory and leave by TMA while the next tile runs.
+// Warps: 0 TMA, 1 TMEM and (leader) MMA, 2 scales, 4-11 promotion (32 rows x 128 columns each). A
+// tile's sums are rounded into shared memory and leave by TMA while the next tile runs.
 // ---------------------------------------------------------------------------------------
 constexpr int PAIR_THREADS = 384;
-constexpr int PAIR_STAGES = 5;
+constexpr int PAIR_STAGES = 4;
 constexpr int PAIR_A_BYTES = 128 * MM_BK;
 constexpr int PAIR_STAGE_BYTES = 2 * 128 * MM_BK;   // this CTA's halves of A and B
-constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 1;
+constexpr int PAIR_GROUPS = 4;                      // ring of scales, four blocks each
+constexpr int PAIR_SCALES = 130;                    // float4: 128 rows, two blocks of columns
+constexpr int PAIR_BARS = 2 * PAIR_STAGES + 4 + 2 * PAIR_GROUPS + 1;
 constexpr int PAIR_SLICE = 32 * 128;                // 128 bytes of 32 rows, 128-byte swizzle
 constexpr int PAIR_OUT = 8 * 2 * PAIR_SLICE;        // two slices per promotion warp
 constexpr size_t PAIR_SMEM = 1024 + (size_t)PAIR_STAGES * PAIR_STAGE_BYTES + PAIR_OUT +
-                             8 * PAIR_BARS + 64;
+                             sizeof(float4) * PAIR_GROUPS * PAIR_SCALES + 8 * PAIR_BARS + 64;
 static_assert(PAIR_SMEM <= 232448, "fits the shared memory of one CTA");
 constexpr int PAIR_GROUP = 8;   // tile rows that are walked together, column by column
 
@@ -698,28 +702,6 @@ __device__ __forceinline__ void pair_tile(const MmArgs &a, int t, int &tm, int &
     tn = r / h;
     tm = g * PAIR_GROUP + (r - tn * h);
 }
-
-// The two scales of blocks kb .. kb + 3 (those that are there). The product is taken a group of
-// blocks later: taken here it would wait for the loads.
-struct Scales4 {
-    float4 x, y;
-    __device__ __forceinline__ void load(const float *pa, const float *pb, int kb, int nkb, bool vec) {
-        if (vec) {
-            if (kb < nkb) {
-                x = *reinterpret_cast<const float4 *>(pa + kb);
-                y = *reinterpret_cast<const float4 *>(pb + kb);
-            }
-        } else {
-            if (kb < nkb) { x.x = pa[kb]; y.x = pb[kb]; }
-            if (kb + 1 < nkb) { x.y = pa[kb + 1]; y.y = pb[kb + 1]; }
-            if (kb + 2 < nkb) { x.z = pa[kb + 2]; y.z = pb[kb + 2]; }
-            if (kb + 3 < nkb) { x.w = pa[kb + 3]; y.w = pb[kb + 3]; }
-        }
-    }
-    __device__ __forceinline__ float4 product() const {
-        return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
-    }
-};
 
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
                                               uint32_t accumulate) {
@@ -733,6 +715,16 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t dtmem, uint64_t adesc, ui
 // memory first and cost the promotion a thousand cycles a block.
 __device__ __forceinline__ void mm_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The scales of up to four blocks of a row, `left` of them there, to shared memory.
+__device__ __forceinline__ void load_scales(float4 *d, const float *src, int left, bool vec) {
+    if (vec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)), "l"(src) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async4(reinterpret_cast<float *>(d) + i, src + (i < left ? i : 0), i < left);
+    }
 }
 
 // acc += s * the 128 columns at taddr, 32 at a time, the next 32 on their way meanwhile; the
@@ -771,11 +763,14 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(mm_smem) + 1023) & ~uintptr_t(1023));
     unsigned char *out = stages + PAIR_STAGES * PAIR_STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(out + PAIR_OUT);
+    float4 *scales = reinterpret_cast<float4 *>(out + PAIR_OUT);
+    uint64_t *full = reinterpret_cast<uint64_t *>(scales + PAIR_GROUPS * PAIR_SCALES);
     uint64_t *empty = full + PAIR_STAGES;
     uint64_t *acc_full = empty + PAIR_STAGES;   // 2
     uint64_t *acc_empty = acc_full + 2;         // 2
-    uint64_t *mma_done = acc_empty + 2;
+    uint64_t *s_full = acc_empty + 2;
+    uint64_t *s_empty = s_full + PAIR_GROUPS;
+    uint64_t *mma_done = s_empty + PAIR_GROUPS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -787,7 +782,9 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (warp == 0) {
         for (int i = lane; i < PAIR_BARS; i += 32) {
             uint64_t *b = full + i;
-            mbar_init(b, b >= acc_empty && b < mma_done ? 16u : 1u);
+            mbar_init(b, b >= acc_empty && b < s_full ? 16u
+                         : b >= s_empty && b < mma_done ? 8u
+                         : b >= s_full && b < s_empty ? 32u : 1u);
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -855,6 +852,31 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             // all MMAs complete before the TMEM is released
             if (one) tc::mma_commit_pair(mma_done, 0x1);
             mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
+        } else if (warp == 2) {
+            Ring<PAIR_GROUPS> sl;
+            bool ok = true;
+            const bool vec = (a.kb & 3) == 0 &&
+                             ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15u) == 0;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int tm, tn;
+                pair_tile(a, t, tm, tn);
+                const int m0 = tm * 256 + 128 * (int)rank;
+                for (int kb = 0; kb < a.kb; kb += 4, sl.next()) {
+                    ok = mm_wait(&s_empty[sl.i], sl.phase ^ 1u, a.wait_limit, abort_flag, 36);
+                    if (!ok) break;
+                    float4 *d = scales + sl.i * PAIR_SCALES;
+                    // rows and columns behind the last take its scales: what they scale is not stored
+#pragma unroll
+                    for (int j = 0; j < 128; j += 32)
+                        load_scales(d + j + lane, a.sA + (long long)min(m0 + j + lane, a.m - 1) * a.kb + kb,
+                                    a.kb - kb, vec);
+                    if (lane < 2)
+                        load_scales(d + 128 + lane, a.sB + (long long)min(2 * tn + lane, a.nb128 - 1) * a.kb + kb,
+                                    a.kb - kb, vec);
+                    cp_async_arrive(&s_full[sl.i]);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -865,24 +887,23 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         const uint32_t release = tc::map_to_rank(acc_empty, 0);
         uint32_t n = 0;   // blocks so far: accumulator n & 1
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * h);
-        const bool vec = (a.kb & 3) == 0 &&
-                         ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15u) == 0;
+        Ring<PAIR_GROUPS> sl;
         for (int t = pair; t < tiles; t += pairs) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
             const int m0 = tm * 256 + 128 * (int)rank + 32 * q, n0 = tn * 256 + 128 * h;
-            // rows and columns behind the last take its scales: what they scale is not stored
-            const float *pa = a.sA + (long long)min(m0 + lane, a.m - 1) * a.kb;
-            const float *pb = a.sB + (long long)min(2 * tn + h, a.nb128 - 1) * a.kb;
-            Scales4 next = {};
-            next.load(pa, pb, 0, a.kb, vec);
             float acc[128];   // 128 columns of one row
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
 #pragma unroll 1
             for (int kb = 0; kb < a.kb; kb += 4) {
-                const float4 sc = next.product();
-                next.load(pa, pb, kb + 4, a.kb, vec);
+                mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 37);
+                float4 sc = scales[sl.i * PAIR_SCALES + 32 * q + lane];
+                const float4 sb = scales[sl.i * PAIR_SCALES + 128 + h];
+                sc.x *= sb.x; sc.y *= sb.y; sc.z *= sb.z; sc.w *= sb.w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[sl.i]);
+                sl.next();
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (u > 0 && kb + u >= a.kb) break;
