@@ -674,8 +674,9 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 // release of its accumulator, about 840 cycles, then the 1000 W power limit. One CTA per
 // 128 x 256 tile has the shorter way (its commits and arrivals stay on the SM) but moves half as
 // much again; on random data it was 6 % slower. Accumulators of 128 columns, four of them, were
-// slower still: every wait and arrival doubles. 16384 x 2048 x 6144 in 174 us (2370 TFLOP/s, tensor
-// pipe busy 62 % of the time), 204 us in a loop that heats the card to its limit.
+// slower still: every wait and arrival doubles; so were sixteen promotion warps of 64 columns.
+// 16384 x 2048 x 6144 in 174 us (2370 TFLOP/s, tensor pipe busy 62 % of the time), 204 us in a loop
+// that heats the card to its limit.
 //
 // Warps: 0 TMA, 1 TMEM and (leader) MMA, 2 scales, 4-11 promotion (32 rows x 128 columns each). A
 // tile's sums are rounded into shared memory and leave by TMA while the next tile runs.
@@ -1084,14 +1085,15 @@ inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, l
 template <typename TY>
 inline int mm_type(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
                    cudaStream_t s) {
-    // up to 32 rows the narrow kernel: 1 x 2048 x 6144 5.9 us, 32 rows 7.7 us (tile kernel 10.2 us);
+    // up to 32 rows the narrow kernel: 1 x 2048 x 6144 5.1 us, 32 rows 6.9 us (tile kernel 10.2 us);
     // at 64 rows of 6144 x 2048 the tile kernel is ahead, 9.0 us to 11.4 us
     if (a.m <= 16) return mm_narrow<16, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 32) return mm_narrow<32, TY>(A, lda, B, ldb, k, a, s);
     // The tile kernel takes 0.22 us a block, 4.5 us a round of CTAs, 2.5 us for the sum over a
     // cluster; the pair kernel 0.44 us a block, 1 us a tile and 5 us once.
-    // Where rounds are even the larger tile wins: 2048 x 2048 x 6144 27 us to 38 us, 777 x 1500 x 2900
-    // 16 us to 13 us.
+    // Pair to tile: 2048 x 2048 x 6144 26 us to 41, 512 x 6144 x 2048 12.2 to 19.4, 3001 x 2048 x 256
+    // 7.3 to 14.6; 777 x 1500 x 2900 15.0 to 12.4, 1024 x 2048 x 6144 24.3 to 20.8, 128 x 6144 x 2048
+    // 13.0 to 9.7.
     long long tile;
     const int split = mm_split((long long)ceil_div(a.m, 128) * ceil_div(a.n, 128), a.kb, 20, 11, tile);
     const long long tiles = (long long)ceil_div(a.m, 256) * ceil_div(a.n, 256), pairs = device_sm_count() / 2;
