@@ -300,7 +300,7 @@ def kv_cache(n_slots: int, heads: int, head_dim: int, *, fmt: int = GPTQ_CACHE_I
         on = p == "k" or values
         c["codes_" + p] = torch.zeros(n_slots, heads, _row_bytes(fmt, head_dim), dtype=torch.uint8,
                                       device=dev) if on else None
-        c["scales_" + p] = torch.zeros(n_slots, heads, head_dim // group,
+        c["scales_" + p] = torch.zeros(n_slots, heads, head_dim // group, dtype=_F32,
                                        device=dev) if on else None
         c["zeros_" + p] = (torch.zeros(n_slots, heads, head_dim // group, dtype=torch.uint8,
                                        device=dev) if on and fmt != GPTQ_CACHE_E4M3 else None)

@@ -168,3 +168,13 @@ def test_write_refuses_addresses_no_element_starts_at(kw):
 @pytest.mark.parametrize("kw", [dict(K=R, dt=1), dict(V=Q), dict(slots=R), dict(sk=Q)])
 def test_read_refuses_addresses_no_element_starts_at(kw):
     refused("gptq_cache_read", {**READ, **kw}.values())
+
+
+def test_cache_scales_are_fp32_whatever_the_default():
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        c = g.kv_cache(4, 2, 64, device="cpu")
+    finally:
+        torch.set_default_dtype(before)
+    assert c["scales_k"].dtype == c["scales_v"].dtype == torch.float32
