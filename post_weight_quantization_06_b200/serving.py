@@ -187,6 +187,8 @@ def _row_bytes(fmt: int, head_dim: int) -> int:
 def _cache_plane(shape, meta, grid, dev, codes, scales, zeros):
     """Addresses of the codes, scales and zero-points of K or V, checked against the cache: `shape`
     of the codes and `meta` of the others."""
+    if codes is None or scales is None or (grid and zeros is None):
+        raise ValueError("the cache lacks an array for these rows")
     if codes.dtype is not _U8 or scales.dtype is not _F32:
         raise TypeError("codes must be uint8 and scales float32")
     if codes.shape != shape or not codes.is_contiguous():
@@ -314,14 +316,17 @@ def cache_write(cache: dict, K: torch.Tensor, V: torch.Tensor | None, slots: tor
                      c["zeros_k"], c["codes_v"], c["scales_v"], c["zeros_v"], c["claims"])
 
 
-def cache_read(cache: dict, slots: torch.Tensor, *, dtype=torch.bfloat16):
-    """(K, V) of ``slots`` of a ``kv_cache`` in fresh tensors (V None for a cache of keys only);
-    rows of negative slots are zero."""
+def cache_read(cache: dict, slots: torch.Tensor, *, dtype=torch.bfloat16, out=None):
+    """(K, V) of ``slots`` of a ``kv_cache`` (V None for a cache of keys only): in fresh tensors of
+    ``dtype``, rows of negative slots zero, or in the two of ``out``, those rows left as they are.
+    Fresh tensors are cleared first, which takes as long again as a long read."""
     c = cache
-    n, heads, nbytes = c["codes_k"].shape
-    dim = nbytes * 2 if c["fmt"] == GPTQ_CACHE_INT4 else nbytes
-    out = [torch.zeros((slots.shape[0], heads, dim), dtype=dtype, device=slots.device)
-           if c["codes_" + p] is not None else None for p in ("k", "v")]
+    if out is None:
+        n, heads, nbytes = c["codes_k"].shape
+        dim = nbytes * 2 if c["fmt"] == GPTQ_CACHE_INT4 else nbytes
+        out = [torch.zeros((slots.shape[0], heads, dim), dtype=dtype, device=slots.device)
+               if c["codes_" + p] is not None else None for p in ("k", "v")]
+    K, V = out
     gptq_cache_read(slots, c["fmt"], c["group_size"], c["codes_k"], c["scales_k"], c["zeros_k"],
-                    c["codes_v"], c["scales_v"], c["zeros_v"], *out)
-    return tuple(out)
+                    c["codes_v"], c["scales_v"], c["zeros_v"], K, V)
+    return K, V

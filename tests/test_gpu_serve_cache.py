@@ -293,3 +293,20 @@ def test_projection_into_the_cache_and_back(g, fmt):
     judge(Y, A, sA, B, sB, "bf16")
     check_values(k, check_arrays(c, "k", np64(kv[:, :h]), at, fmt, 0), "bf16")
     check_values(v, check_arrays(c, "v", np64(kv[:, h:]), at, fmt, 0), "bf16")
+
+
+def test_reading_into_tensors_of_the_caller(g):
+    c = g.kv_cache(40, 2, 64, fmt=g.GPTQ_CACHE_INT8, group_size=32)
+    K, V = rows(40, 2, 64, "bf16", 8), rows(40, 2, 64, "bf16", 9)
+    g.cache_write(c, K, V, torch.arange(40, device=DEV))
+    at = slots_of(20, 40, 3)
+    at[::3] = -1
+    fresh = g.cache_read(c, at)
+    buf = torch.full((20, 2, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)   # K and V side by side
+    k, v = g.cache_read(c, at, out=(buf[:, 0], buf[:, 1]))
+    g.gptq_sync_status()
+    assert k.data_ptr() == buf.data_ptr()
+    kept = at >= 0
+    for got, want in zip((k, v), fresh):
+        assert torch.equal(got[kept], want[kept])
+        assert (got[~kept] == 7).all() and (want[~kept] == 0).all()

@@ -178,3 +178,16 @@ def test_cache_scales_are_fp32_whatever_the_default():
     finally:
         torch.set_default_dtype(before)
     assert c["scales_k"].dtype == c["scales_v"].dtype == torch.float32
+
+
+def test_binding_refuses_a_cache_that_lacks_an_array():
+    K, at = torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int64)
+    c = g.kv_cache(10, 2, 64, device="cpu", values=False)
+    with pytest.raises(ValueError, match="lacks"):
+        g.cache_write(c, K, K, at)
+    with pytest.raises(ValueError, match="lacks"):
+        g.cache_read(c, at, out=(K, K))
+    with pytest.raises(ValueError, match="lacks"):
+        g.cache_write({**c, "zeros_k": None}, K, None, at)
+    with pytest.raises(ValueError, match="lacks"):
+        g.cache_write({**c, "scales_k": None}, K, None, at)
