@@ -85,6 +85,9 @@ typedef enum {
     GPTQ_CACHE_E4M3 = 2  /* e4m3 codes and a scale, no zero-point */
 } gptq_cache_format;
 
+/* Added to the format of gptq_cache_read: rows without a slot are set to zero. */
+#define GPTQ_CACHE_CLEAR 16
+
 /* Most tokens of one gptq_cache_write call that need no `claims`. */
 #define GPTQ_CACHE_UNCLAIMED 512
 
@@ -128,9 +131,10 @@ GPTQ_API int gptq_cache_write(const void *K, int64_t k_token_stride, int64_t k_h
 
 /*
  * Read rows of a cache back: K[t], V[t] = the values of slot slots[t], rounded once to y_dtype.
- * Arguments as in gptq_cache_write, K and V written (no two heads may overlap). A slot may be named any number of times. A
- * negative slot leaves its row of K and V as it was, and so does a slot not below n_slots, which
- * is reported (GPTQ_ERR_ARG, info = token).
+ * Arguments as in gptq_cache_write, K and V written (no two heads may overlap). A slot may be named
+ * any number of times. A negative slot leaves its row of K and V as it was, and so does a slot not
+ * below n_slots, which is reported (GPTQ_ERR_ARG, info = token); with format + GPTQ_CACHE_CLEAR
+ * both rows are set to zero instead.
  */
 GPTQ_API int gptq_cache_read(const int64_t *slots, int64_t tokens, int64_t n_slots, int heads,
                              int head_dim, int format, int group_size, const void *codes_k,

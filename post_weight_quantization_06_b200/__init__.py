@@ -408,6 +408,6 @@ def quantize_layer(W: torch.Tensor, X: torch.Tensor | None = None, *, H: torch.T
 
 
 from .serving import (  # noqa: E402,F401  (needs the library loaded above)
-    EXPORTED_SERVE, GPTQ_CACHE_E4M3, GPTQ_CACHE_INT4, GPTQ_CACHE_INT8, GPTQ_CACHE_UNCLAIMED,
-    GPTQ_F16, GPTQ_FP8_BLOCK, cache_read, cache_write, fp8_matmul, fp8_quantize, gptq_cache_read,
-    gptq_cache_write, gptq_fp8_matmul, gptq_fp8_quantize, kv_cache)
+    EXPORTED_SERVE, GPTQ_CACHE_CLEAR, GPTQ_CACHE_E4M3, GPTQ_CACHE_INT4, GPTQ_CACHE_INT8,
+    GPTQ_CACHE_UNCLAIMED, GPTQ_F16, GPTQ_FP8_BLOCK, cache_read, cache_write, fp8_matmul,
+    fp8_quantize, gptq_cache_read, gptq_cache_write, gptq_fp8_matmul, gptq_fp8_quantize, kv_cache)

@@ -43,6 +43,7 @@ struct CacheArgs {
     int w;                          // lanes of a unit (write)
     int vec;                        // codes take 16-byte accesses (read)
     int full;                       // every lane has all its vectors, aligned (write)
+    int clear;                      // rows of no slot are set to zero (read)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -329,6 +330,18 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float z, float *f) {
     }
 }
 
+// Zeros in place of unit `rem` of token t (units as in the next kernel). Apart from its loop, where
+// an address taken before the loads, for both uses, cost 1 to 3 %.
+template <typename T, int U>
+__device__ __noinline__ void cache_clear(const CacheArgs &a, int t, uint32_t rem) {
+    const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d, h = a.per_head.div(v);
+    const CachePlane &p = a.p[pl];
+    T *y = static_cast<T *>(p.y) + (long long)t * p.ts + (long long)h * p.hs + 8 * U * (v - h * a.per_head.d);
+    const float zero[8] = {};
+#pragma unroll
+    for (int k = 0; k < U; ++k) store8(y + 8 * k, p.vec != 0, zero);
+}
+
 // One unit is 8 U values; per_token.d units per token over the planes, per_plane.d per plane,
 // per_head.d per head, and per_group.d of them share a scale. U = 2 where heads and groups are
 // multiples of 16: what a unit's place costs is then shared by 16 values, and its 16-bit output
@@ -345,9 +358,9 @@ __global__ void __launch_bounds__(CACHE_THREADS, 8) cache_read_kernel(const __gr
     for (uint32_t u = threadIdx.x; u < units; u += CACHE_THREADS) {
         const uint32_t j = a.per_token.div(u), rem = u - j * a.per_token.d;
         const long long sl = a.slots[t0 + (int)j];
-        if (sl < 0) continue;
-        if (sl >= a.n_slots) {
-            if (rem == 0) report(GPTQ_ERR_ARG, t0 + (int)j);
+        if (sl < 0 || sl >= a.n_slots) {
+            if (sl >= 0 && rem == 0) report(GPTQ_ERR_ARG, t0 + (int)j);
+            if (a.clear) cache_clear<T, U>(a, t0 + (int)j, rem);
             continue;
         }
         const uint32_t pl = a.per_plane.div(rem), v = rem - pl * a.per_plane.d;

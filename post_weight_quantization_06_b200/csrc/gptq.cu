@@ -954,6 +954,8 @@ static int gptq_cache_read_body(const int64_t *slots, int64_t tokens, int64_t n_
                                 gptq_stream_t stream) {
     serve::CacheArgs a;
     if (!serve::serve_dtype_ok(y_dtype)) return GPTQ_ERR_ARG;
+    const int clear = format > 0 ? format & GPTQ_CACHE_CLEAR : 0;
+    format -= clear;
     if (int st = cache_check(a, slots, tokens, n_slots, heads, head_dim, format, group_size, codes_k,
                              scales_k, zeros_k, codes_v, scales_v, zeros_v, V != nullptr))
         return st;
@@ -962,6 +964,7 @@ static int gptq_cache_read_body(const int64_t *slots, int64_t tokens, int64_t n_
     if (V && !rows_apart(tokens, heads, head_dim, v_token_stride, v_head_stride)) return GPTQ_ERR_ARG;
     if (off(K, serve::serve_dtype_bytes(y_dtype)) || off(V, serve::serve_dtype_bytes(y_dtype)))
         return GPTQ_ERR_ARG;
+    a.clear = clear;
     a.p[0].y = K;
     a.p[0].ts = k_token_stride;
     a.p[0].hs = k_head_stride;

@@ -17,6 +17,7 @@ GPTQ_F16 = 2
 GPTQ_FP8_BLOCK = 128
 GPTQ_CACHE_INT4, GPTQ_CACHE_INT8, GPTQ_CACHE_E4M3 = 0, 1, 2
 GPTQ_CACHE_UNCLAIMED = 512
+GPTQ_CACHE_CLEAR = 16
 
 EXPORTED_SERVE = ("gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_cache_write", "gptq_cache_read")
 
@@ -277,9 +278,10 @@ def gptq_cache_read(slots: torch.Tensor, fmt: int, group_size: int, codes_k: tor
                     zeros_v: torch.Tensor | None, K: torch.Tensor, V: torch.Tensor | None,
                     stream=None):
     """K, V (tokens x heads x head_dim, written) = the values of the cache's ``slots``. Rows of
-    negative slots are left as they are."""
-    dev, n, (t, h, d), k, v, planes = _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k,
-                                                  zeros_k, codes_v, scales_v, zeros_v)
+    negative slots are left as they are, or zero with ``fmt + GPTQ_CACHE_CLEAR``."""
+    dev, n, (t, h, d), k, v, planes = _cache_args(K, V, slots, fmt & ~GPTQ_CACHE_CLEAR, group_size,
+                                                  codes_k, scales_k, zeros_k, codes_v, scales_v,
+                                                  zeros_v)
     st = _cache_read(slots.data_ptr(), t, n, h, d, fmt, group_size, *planes, *k, *v, _code(K),
                      _stream_of(stream, dev))
     if st:
@@ -318,15 +320,16 @@ def cache_write(cache: dict, K: torch.Tensor, V: torch.Tensor | None, slots: tor
 
 def cache_read(cache: dict, slots: torch.Tensor, *, dtype=torch.bfloat16, out=None):
     """(K, V) of ``slots`` of a ``kv_cache`` (V None for a cache of keys only): in fresh tensors of
-    ``dtype``, rows of negative slots zero, or in the two of ``out``, those rows left as they are.
-    Fresh tensors are cleared first, which takes as long again as a long read."""
+    ``dtype``, rows of negative slots zero, or in the two of ``out``, those rows left as they are."""
     c = cache
+    fmt = c["fmt"]
     if out is None:
         n, heads, nbytes = c["codes_k"].shape
-        dim = nbytes * 2 if c["fmt"] == GPTQ_CACHE_INT4 else nbytes
-        out = [torch.zeros((slots.shape[0], heads, dim), dtype=dtype, device=slots.device)
+        dim = nbytes * 2 if fmt == GPTQ_CACHE_INT4 else nbytes
+        out = [torch.empty((slots.shape[0], heads, dim), dtype=dtype, device=slots.device)
                if c["codes_" + p] is not None else None for p in ("k", "v")]
+        fmt += GPTQ_CACHE_CLEAR
     K, V = out
-    gptq_cache_read(slots, c["fmt"], c["group_size"], c["codes_k"], c["scales_k"], c["zeros_k"],
+    gptq_cache_read(slots, fmt, c["group_size"], c["codes_k"], c["scales_k"], c["zeros_k"],
                     c["codes_v"], c["scales_v"], c["zeros_v"], K, V)
     return K, V

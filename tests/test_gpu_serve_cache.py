@@ -310,3 +310,30 @@ def test_reading_into_tensors_of_the_caller(g):
     for got, want in zip((k, v), fresh):
         assert torch.equal(got[kept], want[kept])
         assert (got[~kept] == 7).all() and (want[~kept] == 0).all()
+
+
+@pytest.mark.parametrize("fmt,dim,group", [(0, 72, 24), (1, 128, 32), (2, 80, 0)])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("pitch", [0, 8, 3])   # heads that follow each other, apart, and unaligned
+def test_clearing_the_rows_without_a_slot(g, fmt, dim, group, dtype, pitch):
+    c = g.kv_cache(30, 3, dim, fmt=fmt, group_size=group)
+    K = rows(30, 3, dim, "fp32", 4)
+    g.cache_write(c, K, K, torch.arange(30, device=DEV))
+    g.gptq_sync_status()
+    at = slots_of(20, 30, 5)
+    at[::3], at[1] = -1, -(1 << 40)
+    fresh = g.cache_read(c, at, dtype=DT[dtype])
+    buf = torch.full((2, 20, 3, dim + pitch), 7.0, dtype=DT[dtype], device=DEV)
+    args = [c[n] for n in ("codes_k", "scales_k", "zeros_k", "codes_v", "scales_v", "zeros_v")]
+    g.gptq_cache_read(at, fmt + g.GPTQ_CACHE_CLEAR, group, *args, buf[0, ..., :dim], buf[1, ..., :dim])
+    g.gptq_sync_status()
+    kept = at >= 0
+    for got, want in zip(buf, fresh):
+        assert (got[..., dim:] == 7).all()
+        assert torch.equal(got[..., :dim], want)
+        assert (want[~kept] == 0).all() and (want[kept] != 0).any()
+    at[4] = 30   # behind the last slot: zero as well, and reported
+    k, _ = g.cache_read(c, at, dtype=DT[dtype])
+    with pytest.raises(g.GptqError):
+        g.gptq_sync_status()
+    assert (k[4] == 0).all() and torch.equal(k[5:], fresh[0][5:])

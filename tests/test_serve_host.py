@@ -191,3 +191,16 @@ def test_binding_refuses_a_cache_that_lacks_an_array():
         g.cache_write({**c, "zeros_k": None}, K, None, at)
     with pytest.raises(ValueError, match="lacks"):
         g.cache_write({**c, "scales_k": None}, K, None, at)
+
+
+@pytest.mark.parametrize("fmt", [19, 16 - 1, 32, 33, 16 + 32, -16])
+def test_read_refuses_formats_it_does_not_know(fmt):
+    refused("gptq_cache_read", {**READ, "fmt": fmt}.values())
+
+
+def test_clearing_belongs_to_reading():
+    src = open(os.path.join(ROOT, "include", "gptq_serve.h")).read()
+    assert f"#define GPTQ_CACHE_CLEAR {g.GPTQ_CACHE_CLEAR}" in src
+    refused("gptq_cache_write", {**WRITE, "fmt": 1 + g.GPTQ_CACHE_CLEAR}.values())
+    refused("gptq_cache_read", {**READ, "fmt": 1 + g.GPTQ_CACHE_CLEAR, "tokens": 0, "K": None}.values(), 0)
+    refused("gptq_cache_read", {**READ, "fmt": 1 + g.GPTQ_CACHE_CLEAR, "zk": None}.values())
