@@ -890,11 +890,14 @@ static int cache_check(serve::CacheArgs &a, const int64_t *slots, int64_t tokens
     }
     return GPTQ_OK;
 }
-// Whether the heads of all tokens lie apart from one another (what is written has to).
+// Whether the heads of all tokens lie apart from one another (what is written has to), within what
+// 64 bits address.
 static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
-    if (tokens == 1) return heads == 1 || hs >= dim;
-    if (heads == 1) return ts >= dim;
-    return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
+    const __int128 t = tokens > 1 ? ts : 0, h = heads > 1 ? hs : 0;
+    if ((tokens - 1) * t + (heads - 1) * h >= (__int128)1 << 60) return false;
+    if (tokens == 1) return heads == 1 || h >= dim;
+    if (heads == 1) return t >= dim;
+    return (h >= dim && t >= (heads - 1) * h + dim) || (t >= dim && h >= (tokens - 1) * t + dim);
 }
 // How wide accesses to rows of x may be: 0 one value, 1 16 bytes, 2 32 bytes.
 static int cache_vec(const void *x, int64_t ts, int64_t hs, int dtype) {

@@ -204,3 +204,9 @@ def test_clearing_belongs_to_reading():
     refused("gptq_cache_write", {**WRITE, "fmt": 1 + g.GPTQ_CACHE_CLEAR}.values())
     refused("gptq_cache_read", {**READ, "fmt": 1 + g.GPTQ_CACHE_CLEAR, "tokens": 0, "K": None}.values(), 0)
     refused("gptq_cache_read", {**READ, "fmt": 1 + g.GPTQ_CACHE_CLEAR, "zk": None}.values())
+
+
+@pytest.mark.parametrize("kt,kh", [(1 << 62, 1 << 62), (1 << 62, 1 << 61), ((1 << 63) - 1, (1 << 63) - 1)])
+def test_read_refuses_strides_whose_products_pass_64_bits(kt, kh):
+    refused("gptq_cache_read", {**READ, "kt": kt, "kh": kh}.values())
+    refused("gptq_cache_read", {**READ, "heads": 4, "V": None, "kt": kt, "kh": kh}.values())
