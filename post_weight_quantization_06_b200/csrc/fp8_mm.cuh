@@ -72,10 +72,29 @@ __device__ __forceinline__ bool mm_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for the phase with this parity. False, with the abort flag set, if `limit` cycles pass
-// first (recorded with `site`) or another role gave up.
+// Waits for the phase with this parity, called by a whole warp. False, with the abort flag set, if
+// `limit` cycles pass first (recorded with `site`) or another role gave up. The answer is the same in
+// every lane: what follows are loops that a warp leaves together and instructions that want all its
+// lanes.
 __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, long long limit,
                                         volatile int *abort_flag, int site) {
+    const uint32_t addr = smem_u32(bar);
+    if (__all_sync(0xffffffffu, mm_try(addr, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mm_try(addr, parity))) {
+        const bool late = clock64() - t0 > limit;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late) report(GPTQ_ERR_TIMEOUT, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// The same for one lane, whose warp does not go by the answer and meets before anything that wants
+// all its lanes (a vote in the pair kernel's promotion cost 3 %).
+__device__ __forceinline__ bool mm_wait_lane(uint64_t *bar, uint32_t parity, long long limit,
+                                             volatile int *abort_flag, int site) {
     const uint32_t addr = smem_u32(bar);
     if (mm_try(addr, parity)) return true;
     const long long t0 = clock64();
@@ -89,8 +108,20 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, long lon
     }
     return true;
 }
-// After an abort: copies in flight land within microseconds, before the shared memory goes away.
-__device__ __forceinline__ void mm_drain() {
+// The issuer's last wait: all its MMAs are complete, after an abort too, before the TMEM is released.
+__device__ __forceinline__ void mm_wait_mmas(uint64_t *mma_done, long long limit, volatile int *abort_flag,
+                                             int site) {
+    const uint32_t addr = smem_u32(mma_done);
+    if (mm_try(addr, 0)) return;
+    if (tc::mbar_wait(mma_done, 0, limit)) return;
+    report(GPTQ_ERR_TIMEOUT, site);
+    *abort_flag = 1;
+}
+// After an abort, once all roles have met: copies in flight land within microseconds, before the
+// shared memory is used for something else or goes away. (The producer cannot say whether there are
+// any: it may have left long before another role gave up.)
+__device__ __forceinline__ void mm_drain(volatile int *abort_flag) {
+    if (!*abort_flag) return;
     const long long t0 = clock64();
     while (clock64() - t0 < 2000000) { }
 }
@@ -236,6 +267,7 @@ struct MmArgs {
     int tiles_m, tiles_n;
     int split;               // CTAs of a cluster, each with a part of the K blocks
     int vec, vec16;          // four values can be stored at once; TMA takes the rows of Y
+    int stall_at, stall_n;   // test hook: barriers whose phases want one arrival too many
     long long wait_limit;
 };
 
@@ -302,7 +334,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             const uint32_t count = (b >= acc_empty && b < s_full) || (b >= s_empty && b < mma_done)
                                        ? 4u
                                        : (b >= s_full && b < s_empty) ? 32u : 1u;
-            mbar_init(b, count);
+            mbar_init(b, count + ((unsigned)(i - a.stall_at) < (unsigned)a.stall_n));
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -328,10 +360,8 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     if (warp == 0) {
         const bool one = elect_one();
         Ring<S::STAGES> st;
-        bool ok = true;
         for (int it = 0; it < nb; ++it, st.next()) {
-            ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 11);
-            if (!ok) break;
+            if (!mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 11)) break;
             if (one) {
                 unsigned char *w = stages + st.i * S::STAGE_BYTES;
                 mbar_expect_tx(&full[st.i], S::STAGE_BYTES);
@@ -340,7 +370,6 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             }
             __syncwarp();
         }
-        if (!ok) mm_drain();
     } else if (warp == 1) {
         const bool one = elect_one();
         Ring<S::STAGES> st;
@@ -363,7 +392,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
             __syncwarp();
         }
         if (one) mma_commit(mma_done);
-        mm_wait(mma_done, 0, a.wait_limit, abort_flag, 14);
+        mm_wait_mmas(mma_done, a.wait_limit, abort_flag, 14);
     } else if (warp == 6) {
         Ring<MM_SCALE_SLOTS> sl;
         const float *sw = a.sB + (long long)tn * a.kb + b0;
@@ -449,6 +478,7 @@ fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    mm_drain(abort_flag);
     if (warp == 1) tmem_dealloc(tmem, S::TMEM);
 }
 
@@ -504,7 +534,7 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             uint64_t *b = full + i;
             const uint32_t count = (b >= acc_empty && b < s_full) || (b >= s_empty && b < mma_done)
                                        ? 8u : (b >= s_full && b < s_empty) ? 32u : 1u;
-            mbar_init(b, count);
+            mbar_init(b, count + ((unsigned)(i - a.stall_at) < (unsigned)a.stall_n));
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -527,10 +557,8 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (warp == 0) {
         const bool one = elect_one();
         Ring<TILE_STAGES> st;
-        bool ok = true;
         for (int it = 0; it < nb; ++it, st.next()) {
-            ok = mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 21);
-            if (!ok) break;
+            if (!mm_wait(&empty[st.i], st.phase ^ 1u, a.wait_limit, abort_flag, 21)) break;
             if (one) {
                 unsigned char *sa = stages + st.i * TILE_STAGE_BYTES;
                 mbar_expect_tx(&full[st.i], TILE_STAGE_BYTES);
@@ -539,7 +567,6 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             }
             __syncwarp();
         }
-        if (!ok) mm_drain();
     } else if (warp == 1) {
         const bool one = elect_one();
         Ring<TILE_STAGES> st;
@@ -562,7 +589,7 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             __syncwarp();
         }
         if (one) mma_commit(mma_done);
-        mm_wait(mma_done, 0, a.wait_limit, abort_flag, 24);
+        mm_wait_mmas(mma_done, a.wait_limit, abort_flag, 24);
     } else if (warp == 2) {
         Ring<MM_SCALE_SLOTS> sl;
         for (int it = 0; it < nb; ++it, sl.next()) {
@@ -605,13 +632,15 @@ fp8_mm_tile_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             for (int j = 0; j < 16; ++j) fma2(acc[16 + j], r1[2 * j], r1[2 * j + 1], s2);
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    mm_drain(abort_flag);
     if (warp == 1) tmem_dealloc(tmem, 512);
 
-    // Sums by row through shared memory (the stages are free: every copy was waited for and every
-    // MMA is done), then whole rows to Y. Row i belongs to CTA i % split of the cluster.
+    // Sums by row through shared memory (the stages are free: every copy was waited for or drained and
+    // every MMA is done), then whole rows to Y. Row i belongs to CTA i % split of the cluster.
     float *sum = reinterpret_cast<float *>(stages);
     const int own = (128 + a.split - 1) / a.split;
     if (a.split > 1) cluster_sync_all();
@@ -783,9 +812,10 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (warp == 0) {
         for (int i = lane; i < PAIR_BARS; i += 32) {
             uint64_t *b = full + i;
-            mbar_init(b, b >= acc_empty && b < s_full ? 16u
-                         : b >= s_empty && b < mma_done ? 8u
-                         : b >= s_full && b < s_empty ? 32u : 1u);
+            const uint32_t count = b >= acc_empty && b < s_full ? 16u
+                                   : b >= s_empty && b < mma_done ? 8u
+                                   : b >= s_full && b < s_empty ? 32u : 1u;
+            mbar_init(b, count + ((unsigned)(i - a.stall_at) < (unsigned)a.stall_n));
         }
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -826,7 +856,6 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                     __syncwarp();
                 }
             }
-            if (!ok) mm_drain();
         } else if (warp == 1 && rank == 0) {
             const bool one = elect_one();
             Ring<PAIR_STAGES> st;
@@ -852,7 +881,7 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             }
             // all MMAs complete before the TMEM is released
             if (one) tc::mma_commit_pair(mma_done, 0x1);
-            mm_wait(mma_done, 0, a.wait_limit, abort_flag, 34);
+            mm_wait_mmas(mma_done, a.wait_limit, abort_flag, 34);
         } else if (warp == 2) {
             Ring<PAIR_GROUPS> sl;
             bool ok = true;
@@ -898,7 +927,7 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
 #pragma unroll 1
             for (int kb = 0; kb < a.kb; kb += 4) {
-                mm_wait(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 37);
+                mm_wait_lane(&s_full[sl.i], sl.phase, a.wait_limit, abort_flag, 37);
                 float4 sc = scales[sl.i * PAIR_SCALES + 32 * q + lane];
                 const float4 sb = scales[sl.i * PAIR_SCALES + 128 + h];
                 sc.x *= sb.x; sc.y *= sb.y; sc.z *= sb.z; sc.w *= sb.w;
@@ -910,7 +939,7 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                     if (u > 0 && kb + u >= a.kb) break;
                     // no way out after an abort (its later waits return at once): a branch that
                     // leaves the loop made the compiler move the 128 sums about
-                    mm_wait(&acc_full[n & 1], (n >> 1) & 1, a.wait_limit, abort_flag, 35);
+                    mm_wait_lane(&acc_full[n & 1], (n >> 1) & 1, a.wait_limit, abort_flag, 35);
                     pair_promote(tq + (n & 1) * 256, u == 0 ? sc.x : u == 1 ? sc.y : u == 2 ? sc.z : sc.w,
                                  acc, release + 8 * (n & 1), lane);
                     ++n;
@@ -953,6 +982,7 @@ fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    mm_drain(abort_flag);
     cluster_sync_all();  // the peer's TMEM, barriers and shared memory outlive every access
     tc_fence_after();
     if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
@@ -1035,6 +1065,17 @@ inline int mm_split(long long tiles, int kb, int round, int add, long long &cost
     return best;
 }
 
+// Test hook: kind `a.stall_n` of barrier (1 accumulator full, 2 stage full, 3 stage empty, 4 scales full,
+// 5 accumulator empty; 0 none) as the range of a kernel's barriers, which lie in this order: stages full and
+// empty, accumulators full and empty, scales full and empty.
+inline void mm_stall(MmArgs &a, int stages, int bufs, int slots) {
+    const int at[6] = {0, 2 * stages, 0, stages, 2 * stages + 2 * bufs, 2 * stages + bufs};
+    const int n[6] = {0, bufs, stages, stages, slots, bufs};
+    const int kind = a.stall_n > 0 && a.stall_n < 6 ? a.stall_n : 0;
+    a.stall_at = at[kind];
+    a.stall_n = n[kind];
+}
+
 template <int NT, typename TY>
 inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb, long long k,
                      MmArgs a, cudaStream_t s) {
@@ -1043,6 +1084,7 @@ inline int mm_narrow(const void *A, long long lda, const void *B, long long ldb,
     a.tiles_n = ceil_div(a.n, 128);
     long long cost;   // a block 0.24 us, a round 3 us, the sum over the cluster 0.5 us
     a.split = mm_split((long long)a.tiles_n * a.tiles_m, a.kb, 12, 2, cost);
+    mm_stall(a, S::STAGES, S::BUFS, MM_SCALE_SLOTS);
     CUtensorMap wmap, xmap;
     if (!mm_map(&wmap, B, a.n, k, ldb, 128) || !mm_map(&xmap, A, a.m, k, lda, NT)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_narrow_kernel<NT, TY>;
@@ -1057,6 +1099,7 @@ inline int mm_tile(const void *A, long long lda, const void *B, long long ldb, l
     a.tiles_m = ceil_div(a.m, 128);
     a.tiles_n = ceil_div(a.n, 128);
     a.split = split;
+    mm_stall(a, TILE_STAGES, TILE_BUFS, MM_SCALE_SLOTS);
     CUtensorMap amap, bmap;
     if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
     auto kernel = fp8_mm_tile_kernel<TY>;
@@ -1073,6 +1116,7 @@ inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, l
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
     if (tiles > 0x7fffffffLL - 1024) return GPTQ_ERR_ARG;
     a.split = 1;
+    mm_stall(a, PAIR_STAGES, 2, PAIR_GROUPS);
     CUtensorMap amap, bmap, ymap = {};
     if (!mm_map(&amap, A, a.m, k, lda, 128) || !mm_map(&bmap, B, a.n, k, ldb, 128)) return GPTQ_ERR_CUDA;
     if (a.vec16 && !mm_out_map<TY>(&ymap, a)) return GPTQ_ERR_CUDA;
@@ -1123,6 +1167,7 @@ inline int fp8_matmul(const void *A, long long lda, const float *sA, const void 
     // a wait longer than ~2 s at the 1.9 GHz clock means a lost signal, not a slow kernel
     static const long long wait_limit = tc::env_ll("GPTQ_WAIT_LIMIT_CYCLES", 4000000000LL);
     a.wait_limit = wait_limit;
+    a.stall_n = (int)tc::env_ll("GPTQ_TEST_STALL", 0);   // made a range of barriers by mm_stall
     switch (y_dtype) {
         case GPTQ_BF16: return mm_type<__nv_bfloat16>(A, lda, B, ldb, k, a, s);
         case GPTQ_F16: return mm_type<__half>(A, lda, B, ldb, k, a, s);
