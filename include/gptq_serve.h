@@ -130,7 +130,8 @@ GPTQ_API int gptq_cache_write(const void *K, int64_t k_token_stride, int64_t k_h
                               gptq_stream_t stream);
 
 /*
- * Read rows of a cache back: K[t], V[t] = the values of slot slots[t], rounded once to y_dtype.
+ * Read rows of a cache back: K[t], V[t] = the values of slot slots[t], each the product s (code - z)
+ * (e4m3: s times the code's value) rounded to fp32 and, where y_dtype has 16 bits, rounded to it next.
  * Arguments as in gptq_cache_write, K and V written (no two heads may overlap). A slot may be named
  * any number of times. A negative slot leaves its row of K and V as it was, and so does a slot not
  * below n_slots, which is reported (GPTQ_ERR_ARG, info = token); with format + GPTQ_CACHE_CLEAR

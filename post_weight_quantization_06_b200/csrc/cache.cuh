@@ -298,7 +298,10 @@ __device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b)
                  "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                  : "memory");
 }
-// Eight values of one word (4 bits) or two (8 bits).
+// Eight values of one word (4 bits) or two (8 bits), in fp32. An output of 16 bits rounds them a second
+// time: 0 to 9 of 100000 values then come out one step from the nearest one. A sticky last bit, as the
+// quantizer has it, would avoid that at four instructions a value instead of one: 131072 tokens of
+// 8 x 128 at 8 bits 137 us, 127 us without; 8192 tokens at 4 bits 10.8 and 8.9 us.
 template <int FMT>
 __device__ __forceinline__ void decode8(uint2 c, float s, float z, float *f) {
     if (FMT == GPTQ_CACHE_E4M3) {

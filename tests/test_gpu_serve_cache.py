@@ -337,3 +337,19 @@ def test_clearing_the_rows_without_a_slot(g, fmt, dim, group, dtype, pitch):
     with pytest.raises(g.GptqError):
         g.gptq_sync_status()
     assert (k[4] == 0).all() and torch.equal(k[5:], fresh[0][5:])
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("dim,group", [(128, 32), (72, 24)])
+def test_values_are_rounded_to_fp32_and_then_to_the_output(g, fmt, dim, group):
+    n = 500
+    c = g.kv_cache(n, 4, dim, fmt=fmt, group_size=group)
+    at = torch.arange(n, device=DEV)
+    g.cache_write(c, rows(n, 4, dim, "fp32", 1), rows(n, 4, dim, "fp32", 2), at)
+    wide = g.cache_read(c, at, dtype=torch.float32)
+    for dtype in ("bf16", "fp16"):
+        for got, want in zip(g.cache_read(c, at, dtype=DT[dtype]), wide):
+            assert torch.equal(got, want.to(DT[dtype]))
+    q = serve.cache_quantize(np64(rows(n, 4, dim, "fp32", 1)), BITS[fmt], group)
+    assert np.array_equal(wide[0].cpu().numpy(), q["values"].astype(np.float32))
+    g.gptq_sync_status()
