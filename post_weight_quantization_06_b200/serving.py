@@ -223,6 +223,8 @@ def _cache_args(K, V, slots, fmt, group_size, codes_k, scales_k, zeros_k, codes_
     kt, kh, one = K.stride()
     if one != 1 and d > 1:
         raise ValueError("K: the values of a head must be contiguous")
+    if codes_k is None:
+        raise ValueError("the cache lacks an array for these rows")
     n = codes_k.shape[0]
     if group_size < 0 or (group_size and d % group_size):
         raise ValueError("group_size must divide head_dim")
@@ -324,6 +326,8 @@ def cache_read(cache: dict, slots: torch.Tensor, *, dtype=torch.bfloat16, out=No
     c = cache
     fmt = c["fmt"]
     if out is None:
+        if c["codes_k"] is None:
+            raise ValueError("the cache lacks an array for these rows")
         n, heads, nbytes = c["codes_k"].shape
         dim = nbytes * 2 if fmt == GPTQ_CACHE_INT4 else nbytes
         out = [torch.empty((slots.shape[0], heads, dim), dtype=dtype, device=slots.device)

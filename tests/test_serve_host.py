@@ -210,3 +210,12 @@ def test_clearing_belongs_to_reading():
 def test_read_refuses_strides_whose_products_pass_64_bits(kt, kh):
     refused("gptq_cache_read", {**READ, "kt": kt, "kh": kh}.values())
     refused("gptq_cache_read", {**READ, "heads": 4, "V": None, "kt": kt, "kh": kh}.values())
+
+
+def test_binding_refuses_a_cache_without_codes_of_keys():
+    K, at = torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int64)
+    c = {**g.kv_cache(10, 2, 64, device="cpu"), "codes_k": None}
+    for call in (lambda: g.cache_write(c, K, K, at), lambda: g.cache_read(c, at),
+                 lambda: g.cache_read(c, at, out=(K, K))):
+        with pytest.raises(ValueError, match="lacks"):
+            call()
