@@ -299,7 +299,7 @@ def kv_cache(n_slots: int, heads: int, head_dim: int, *, fmt: int = GPTQ_CACHE_I
     _want(head_dim > 0 and head_dim % 8 == 0 and 0 < group <= 1024 and group % 8 == 0
           and head_dim % group == 0, "head_dim and group_size must be multiples of 8, and groups "
                                      "of at most 1024 fill a head")
-    dev = device or "cuda"
+    dev = "cuda" if device is None else device
     c = dict(fmt=fmt, group_size=group_size,
              claims=torch.zeros(n_slots, dtype=torch.int32, device=dev))
     for p in ("k", "v"):

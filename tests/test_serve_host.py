@@ -219,3 +219,15 @@ def test_binding_refuses_a_cache_without_codes_of_keys():
                  lambda: g.cache_read(c, at, out=(K, K))):
         with pytest.raises(ValueError, match="lacks"):
             call()
+
+
+@pytest.mark.parametrize("device,want", [(0, 0), (1, 1), ("cpu", "cpu"), (None, "cuda")])
+def test_a_cache_lies_on_the_device_that_was_named(monkeypatch, device, want):
+    seen, zeros = [], torch.zeros
+
+    def on_the_host(*shape, device=None, **kw):
+        seen.append(device)
+        return zeros(*shape, **kw)
+    monkeypatch.setattr(torch, "zeros", on_the_host)
+    g.kv_cache(4, 2, 64, device=device)
+    assert seen and all(type(d) is type(want) and d == want for d in seen)
