@@ -299,6 +299,8 @@ def kv_cache(n_slots: int, heads: int, head_dim: int, *, fmt: int = GPTQ_CACHE_I
     _want(head_dim > 0 and head_dim % 8 == 0 and 0 < group <= 1024 and group % 8 == 0
           and head_dim % group == 0, "head_dim and group_size must be multiples of 8, and groups "
                                      "of at most 1024 fill a head")
+    _want(heads > 0 and heads * head_dim <= 65536, "heads must be positive and heads * head_dim at "
+                                                   "most 65536")
     dev = "cuda" if device is None else device
     c = dict(fmt=fmt, group_size=group_size,
              claims=torch.zeros(n_slots, dtype=torch.int32, device=dev))

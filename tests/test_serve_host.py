@@ -231,3 +231,13 @@ def test_a_cache_lies_on_the_device_that_was_named(monkeypatch, device, want):
     monkeypatch.setattr(torch, "zeros", on_the_host)
     g.kv_cache(4, 2, 64, device=device)
     assert seen and all(type(d) is type(want) and d == want for d in seen)
+
+
+@pytest.mark.parametrize("heads,dim,group", [(0, 64, 0), (-1, 64, 0), (512, 256, 0), (1025, 64, 32)])
+def test_no_cache_is_made_that_the_calls_would_refuse(heads, dim, group):
+    with pytest.raises(ValueError, match="heads"):
+        g.kv_cache(4, heads, dim, group_size=group, device="cpu")
+    refused("gptq_cache_write", {**WRITE, "heads": heads, "dim": dim, "group": group}.values())
+    refused("gptq_cache_read", {**READ, "heads": heads, "dim": dim, "group": group, "kt": 1 << 20,
+                                "kh": dim, "vt": 1 << 20, "vh": dim}.values())
+    assert g.kv_cache(1, 65536 // dim, dim, group_size=group, device="cpu")["codes_k"].shape[1] == 65536 // dim
