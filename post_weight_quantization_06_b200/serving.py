@@ -46,8 +46,11 @@ def _bind():
 _fp8_quantize, _fp8_matmul, _cache_write, _cache_read = _bind()
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# The functions behind torch.cuda.current_device and current_stream, without the objects these make;
+# a torch built without CUDA has neither, and no tensor there reaches them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream_of(stream, dev: int) -> int:

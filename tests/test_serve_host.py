@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -241,3 +242,20 @@ def test_no_cache_is_made_that_the_calls_would_refuse(heads, dim, group):
     refused("gptq_cache_read", {**READ, "heads": heads, "dim": dim, "group": group, "kt": 1 << 20,
                                 "kh": dim, "vt": 1 << 20, "vh": dim}.values())
     assert g.kv_cache(1, 65536 // dim, dim, group_size=group, device="cpu")["codes_k"].shape[1] == 65536 // dim
+
+
+def test_the_package_imports_where_torch_has_no_cuda():
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import post_weight_quantization_06_b200 as g
+try:
+    g.fp8_quantize(torch.zeros(4, 256))
+except ValueError as e:
+    assert "current device" in str(e)
+    print("ok")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.stdout.strip() == "ok", out.stderr[-2000:]
