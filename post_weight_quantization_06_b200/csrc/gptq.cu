@@ -890,19 +890,23 @@ static int cache_check(serve::CacheArgs &a, const int64_t *slots, int64_t tokens
     }
     return GPTQ_OK;
 }
-// Whether the heads of all tokens lie apart from one another (what is written has to), within what
-// 64 bits address.
+// Whether the heads of all tokens lie within what 64 bits address.
+static bool rows_in_reach(int64_t tokens, int64_t heads, int64_t ts, int64_t hs) {
+    const __int128 t = ts < 0 ? -(__int128)ts : ts, h = hs < 0 ? -(__int128)hs : hs;
+    return (tokens - 1) * t + (heads - 1) * h < (__int128)1 << 60;
+}
+// Whether they do, and lie apart from one another (what is written has to).
 static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
-    const __int128 t = tokens > 1 ? ts : 0, h = heads > 1 ? hs : 0;
-    if ((tokens - 1) * t + (heads - 1) * h >= (__int128)1 << 60) return false;
+    if (!rows_in_reach(tokens, heads, ts, hs)) return false;
+    const int64_t t = tokens > 1 ? ts : 0, h = heads > 1 ? hs : 0;
     if (tokens == 1) return heads == 1 || h >= dim;
     if (heads == 1) return t >= dim;
     return (h >= dim && t >= (heads - 1) * h + dim) || (t >= dim && h >= (tokens - 1) * t + dim);
 }
 // How wide accesses to rows of x may be: 0 one value, 1 16 bytes, 2 32 bytes.
 static int cache_vec(const void *x, int64_t ts, int64_t hs, int dtype) {
-    const int64_t size = serve::serve_dtype_bytes(dtype);
-    const uint64_t all = reinterpret_cast<uintptr_t>(x) | (uint64_t)(ts * size) | (uint64_t)(hs * size);
+    const uint64_t size = serve::serve_dtype_bytes(dtype);
+    const uint64_t all = reinterpret_cast<uintptr_t>(x) | (uint64_t)ts * size | (uint64_t)hs * size;
     return all % 32 == 0 ? 2 : all % 16 == 0 ? 1 : 0;
 }
 
@@ -920,6 +924,9 @@ static int gptq_cache_write_body(const void *K, int64_t k_token_stride, int64_t 
         return st;
     if (tokens == 0) return GPTQ_OK;
     if (!K || (tokens > GPTQ_CACHE_UNCLAIMED && !claims)) return GPTQ_ERR_ARG;
+    if (!rows_in_reach(tokens, heads, k_token_stride, k_head_stride) ||
+        (V && !rows_in_reach(tokens, heads, v_token_stride, v_head_stride)))
+        return GPTQ_ERR_ARG;
     if (off(K, serve::serve_dtype_bytes(x_dtype)) || off(V, serve::serve_dtype_bytes(x_dtype)) ||
         off(claims, 4))
         return GPTQ_ERR_ARG;

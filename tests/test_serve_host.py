@@ -259,3 +259,10 @@ except ValueError as e:
 """
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert out.stdout.strip() == "ok", out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("t,h", [(1 << 62, 64), (-(1 << 62), 64), (64, 1 << 60), (1 << 59, 1 << 59),
+                                 (-(1 << 63), 0), ((1 << 63) - 1, -(1 << 63))])
+def test_write_refuses_strides_whose_products_pass_64_bits(t, h):
+    refused("gptq_cache_write", {**WRITE, "kt": t, "kh": h}.values())
+    refused("gptq_cache_write", {**WRITE, "vt": t, "vh": h}.values())
