@@ -70,8 +70,9 @@ GPTQ_API int gptq_fp8_quantize(const void *X, int x_dtype, int64_t rows, int64_t
  *           (ldy >= n). Must not overlap the inputs.
  * A and B must start on 16-byte boundaries, and lda and ldb be multiples of 16, at least k (the
  * pitch of a single row is not looked at). m, n and k are otherwise free (k == 0 writes zeros, m == 0 or n == 0 is a no-op), each < 2^31 - 256.
- * The result of a call depends on its arguments alone (no atomics). It may differ in the last
- * bits between values of m, which choose how the sum over the blocks is split.
+ * A call gives the same bits each time it is made on a device of the same number of multiprocessors
+ * (no atomics). m, n, k and that number choose how the sum over the blocks is split, so the same row or
+ * column can differ in its last bits between products of other sizes, or between devices.
  * A code that is NaN makes its row (A) or column (B) of Y NaN. Scales are taken as they are.
  */
 GPTQ_API int gptq_fp8_matmul(const void *A, int64_t lda, const float *sA, const void *B,

@@ -1043,13 +1043,12 @@ inline int mm_launch(void (*kernel)(P...), long long ctas, int cluster, int thre
     return e == cudaSuccess ? st : GPTQ_ERR_CUDA;
 }
 
-// CTAs with an SM's shared memory that run at once in clusters of `size`, from the occupancy
-// call on a B200 of 148 SMs, whose clusters do not cross the borders of its SM groups: larger
-// clusters leave SMs idle (seven: 105).
+// CTAs with an SM's shared memory that run at once in clusters of `size`: from the occupancy call
+// on a B200 of 148 SMs, whose clusters do not cross the borders of its SM groups (larger clusters
+// leave SMs idle: seven, 105), and in proportion for other counts. It only chooses the parts of K.
 inline int mm_resident(int size) {
     static const int on148[9] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
-    const int sms = device_sm_count();
-    return sms >= 148 ? on148[size] : sms / size * size * 3 / 4;
+    return on148[size] * device_sm_count() / 148;
 }
 // Parts of K for `tiles` tiles: the least cost, rounds of CTAs x (blocks of a CTA and what a round
 // costs besides) and what adding the parts up costs; all in blocks of a CTA.
