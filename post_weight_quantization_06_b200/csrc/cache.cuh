@@ -175,8 +175,15 @@ struct WriteUnit {
     }
 };
 
+// CTAs an SM with V vectors of eight a lane. At 16 bits the min-max forms spill 4 to 24 bytes a thread under
+// these bounds. Five instead of six with V = 4: 2048 tokens of 8 x 128 at 8 bits 6.5 us instead of 7.3, at
+// e4m3 6.3 and 6.6; 32768 tokens 42.8 and 43.2, at e4m3 44.5 and 42.8.
+template <typename T>
+__host__ __device__ constexpr int cache_write_ctas(int V) {
+    return sizeof(T) == 2 ? (V == 4 ? 6 : 5) : (V == 4 ? 4 : 3);
+}
 template <typename T, int FMT, int V>
-__global__ void __launch_bounds__(CACHE_THREADS, sizeof(T) == 2 ? (V == 4 ? 6 : 5) : (V == 4 ? 4 : 3))
+__global__ void __launch_bounds__(CACHE_THREADS, cache_write_ctas<T>(V))
 cache_write_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ long long slot[CACHE_MAX_TB];
     __shared__ int beaten[CACHE_MAX_TB];
@@ -422,13 +429,17 @@ inline int cache_tokens_per_cta(int tokens, long long per_token) {
 template <typename T, int FMT>
 inline int cache_write_launch(CacheArgs &a, cudaStream_t s) {
     // Four or six vectors of eight a lane: what a group costs once (its grid) is shared by up to 48
-    // values. Six in long calls where that leaves fewer of them empty (heads of 80, 96, 192: 32768
-    // tokens of 16 x 80 at 4 bits 73 us with four, 53 us with six; 64 tokens of 8 x 96 3.4 and 3.9 us).
+    // values. Six where that leaves fewer of them empty (heads of 80, 96, 192) and four would take more
+    // lanes than the device holds at once; up to there more lanes are the shorter way. With four and six,
+    // bf16 at 4 bits: 16 x 80, 1024 tokens 7.1 and 7.2 us, 2048 8.8 and 8.2, 32768 76 and 55; 8 x 96, 2048 tokens
+    // 6.9 and 8.0, 8192 13.0 and 11.4; 8 x 192, 1024 tokens 6.6 and 6.6, 2048 8.5 and 7.6. (At 513 tokens
+    // six would be ahead for 8 x 192, 5.5 and 4.8 us, and behind for 8 x 96, 4.3 and 4.5.)
     const int nvec = a.group / 8;
     int w4 = 1, w6 = 1;
     while (4 * w4 < nvec) w4 *= 2;
     while (6 * w6 < nvec) w6 *= 2;
-    const bool six = a.tokens > GPTQ_CACHE_UNCLAIMED && 6 * w6 < 4 * w4;
+    const long long at_once = (long long)device_sm_count() * cache_write_ctas<T>(4) * CACHE_THREADS;
+    const bool six = 6 * w6 < 4 * w4 && (long long)a.tokens * a.per_token.d * w4 > at_once;
     a.w = six ? w6 : w4;
     a.full = nvec == (six ? 6 : 4) * a.w && a.p[0].vec && (!a.p[1].x || a.p[1].vec);
     a.tb = cache_tokens_per_cta(a.tokens, (long long)a.per_token.d * a.w);

@@ -353,3 +353,23 @@ def test_values_are_rounded_to_fp32_and_then_to_the_output(g, fmt, dim, group):
     q = serve.cache_quantize(np64(rows(n, 4, dim, "fp32", 1)), BITS[fmt], group)
     assert np.array_equal(wide[0].cpu().numpy(), q["values"].astype(np.float32))
     g.gptq_sync_status()
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,h,d,group", [(3000, 16, 80, 0), (1100, 16, 80, 0), (9000, 4, 96, 0),
+                                         (2000, 8, 192, 0), (3000, 8, 80, 40), (40000, 1, 40, 0)])
+def test_long_writes_of_heads_that_are_no_power_of_two(g, fmt, dtype, t, h, d, group):
+    """Both widths of a lane, and calls that end inside a CTA; every 97th token against the oracle."""
+    K, V = rows(t, h, d, dtype, 1), rows(t, h, d, dtype, 2)
+    at = slots_of(t, t + 5, 7)
+    at[::5] = -1
+    c = g.kv_cache(t + 5, h, d, fmt=fmt, group_size=group)
+    g.cache_write(c, K, V, at)
+    g.gptq_sync_status()
+    some = torch.arange(1, t, 97, device=DEV)
+    some = torch.cat([some, torch.tensor([t - 1], device=DEV)])
+    some = some[at[some] >= 0]
+    check_arrays(c, "k", np64(K[some]), at[some], fmt, group)
+    check_arrays(c, "v", np64(V[some]), at[some], fmt, group)
+    assert (c["claims"] == 0).all()
