@@ -364,3 +364,71 @@ def test_the_first_calls_of_a_process_can_be_captured():
     out = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True,
                          timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stderr[-2000:]
+
+
+def judge_columns(Y, A, sA, B, sB, dtype, blocks):
+    """`judge` on some blocks of 128 columns."""
+    for j in blocks:
+        at = slice(128 * j, min(128 * j + 128, B.shape[0]))
+        judge(Y[:, at], A, sA, B[at], sB[j:j + 1], dtype)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8192, 8192), (16, 8192, 8192), (20, 8192, 8192), (32, 8064, 8100),
+                                   (1, 128, 40000), (25, 300, 30000)])
+def test_matmul_few_rows_with_many_blocks_a_cta(g, m, n, k):
+    """More blocks of K in a CTA than it has stages, scale slots and accumulators."""
+    ops = operands(g, m, n, k, seed=n + k)
+    Y = g.fp8_matmul(*ops, out_dtype=torch.float32)
+    g.gptq_sync_status()
+    last = (n - 1) // 128
+    judge_columns(Y, *ops, "fp32", sorted({0, last // 2, last}))
+
+
+@pytest.mark.parametrize("m,n,k", [(200, 3000, 3000), (40, 128, 20000), (130, 9000, 1700)])
+def test_matmul_tiles_with_many_blocks_a_cta(g, m, n, k):
+    ops = operands(g, m, n, k, seed=n + k)
+    Y = g.fp8_matmul(*ops, out_dtype=torch.float32)
+    g.gptq_sync_status()
+    last = (n - 1) // 128
+    judge_columns(Y, *ops, "fp32", sorted({0, last // 2, last}))
+
+
+@pytest.mark.parametrize("shift", [0, 1])   # scales that start on 16 bytes, and 4 bytes behind
+@pytest.mark.parametrize("k", [640, 900, 1024, 1700])
+def test_matmul_large_sizes_with_any_number_of_blocks(g, k, shift):
+    m, n = 3000, 2816
+    A, sA, B, sB = operands(g, m, n, k, seed=k)
+    moved = torch.zeros(sA.numel() + shift, device=DEV)
+    moved[shift:] = sA.reshape(-1)
+    sA = moved[shift:].view(sA.shape)
+    assert sA.data_ptr() % 16 == 4 * shift
+    Y = g.fp8_matmul(A, sA, B, sB, out_dtype=torch.float32)
+    g.gptq_sync_status()
+    # rows of the first tiles of a CTA pair and of its later ones
+    at = torch.cat([torch.arange(0, 12), torch.arange(250, 262), torch.arange(2040, 2060),
+                    torch.arange(2980, 3000)]).to(DEV)
+    judge(Y[at], A.view(torch.uint8)[at].view(F8), sA[at], B, sB, "fp32")
+    assert torch.isfinite(Y).all()
+
+
+def test_matmul_nan_stays_in_its_row_and_column_at_large_sizes(g):
+    m, n, k = 3000, 2816, 300
+    A, sA, B, sB = operands(g, m, n, k)
+    A.view(torch.uint8)[2077, 290] = 0x7f
+    B.view(torch.uint8)[1500, 5] = 0xff
+    Y = g.fp8_matmul(A, sA, B, sB, out_dtype=torch.float32)
+    g.gptq_sync_status()
+    want = torch.zeros(m, n, dtype=torch.bool, device=DEV)
+    want[2077] = True
+    want[:, 1500] = True
+    assert torch.equal(torch.isnan(Y), want)
+
+
+def test_the_product_of_one_token_is_the_nearest_to_its_fp32_sums_each_time(g):
+    ops = operands(g, 1, 2048, 6144, seed=4)
+    wide = g.fp8_matmul(*ops, out_dtype=torch.float32)
+    first = g.fp8_matmul(*ops)
+    assert torch.equal(first, wide.to(torch.bfloat16))
+    for _ in range(20):
+        assert torch.equal(g.fp8_matmul(*ops), first)
+    g.gptq_sync_status()
