@@ -277,8 +277,8 @@ struct MmArgs {
 // cluster; each sends its sums to the CTA that owns the token, which adds them in the order of
 // the parts. (64 rows a CTA, to split less, took as long or longer at every size tried.) Bytes of
 // the weight should bound it; at one token what a launch costs from its set-up to the exchange in
-// the cluster does: 1 x 2048 x 6144 in 5.1 us (2.5 TB/s; an empty launch of this shape 3 us), 1 x 8192 x
-// 8192 in 14 us (4.7 TB/s).
+// the cluster does: 1 x 2048 x 6144 in 5.2 us with the weight in the L2, 6.2 us from DRAM (2.0 TB/s; an empty launch of
+// this shape 3 us), 1 x 8192 x 8192 in 12 and 15 us (4.4 TB/s).
 //
 // Warps: 0 TMA, 1 TMEM and MMA, 2-5 promotion (32 weight rows each), 6 scales.
 // ---------------------------------------------------------------------------------------
@@ -1128,8 +1128,8 @@ inline int mm_pair(const void *A, long long lda, const void *B, long long ldb, l
 template <typename TY>
 inline int mm_type(const void *A, long long lda, const void *B, long long ldb, long long k, MmArgs a,
                    cudaStream_t s) {
-    // up to 32 rows the narrow kernel: 1 x 2048 x 6144 5.1 us, 32 rows 6.9 us (tile kernel 10.2 us);
-    // at 64 rows of 6144 x 2048 the tile kernel is ahead, 9.0 us to 11.4 us
+    // up to 32 rows the narrow kernel: 1 x 2048 x 6144 5.2 us, 32 rows 7.0 us (tile kernel 10.3 us);
+    // at 64 rows of 6144 x 2048 the tile kernel is ahead, 9.1 us to 11.4 us
     if (a.m <= 16) return mm_narrow<16, TY>(A, lda, B, ldb, k, a, s);
     if (a.m <= 32) return mm_narrow<32, TY>(A, lda, B, ldb, k, a, s);
     // The tile kernel takes 0.22 us a block, 4.5 us a round of CTAs, 2.5 us for the sum over a
